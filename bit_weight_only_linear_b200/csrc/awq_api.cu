@@ -16,6 +16,8 @@
 #include "gemm_sm100.cuh"
 #include "search.cuh"
 #include "clip.cuh"
+#include "linear_simple.cuh"
+#include "moe.cuh"
 
 using namespace awq;
 
@@ -267,6 +269,109 @@ awq_status awq_scale_search_noalloc(const uint16_t* X, int32_t M, const uint16_t
     if (L.nc <= 0) return AWQ_ERR_UNSUPPORTED;
     return run_scale_search_chunked(X, M, W, N, K, cfg.q_group_size, cfg.zero_point, n_grid, s_out, losses_out,
                                     best_index_out, L, (cudaStream_t)stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the fused and the grouped linear; the row counts may be 0.
+awq_status check_fused(const uint16_t* X, int M, int64_t ldx, const uint32_t* qweight, const uint16_t* scales,
+                       const uint32_t* qzeros, int N, int K, const awq_quant_config& cfg, const uint16_t* bias,
+                       int activation, int gated, const uint16_t* residual, int64_t ldr, const uint16_t* Y,
+                       int64_t ldy, bool empty) {
+    awq_status st = check_config(cfg);
+    if (st != AWQ_OK) return st;
+    st = check_shape(N, K, cfg);
+    if (st != AWQ_OK) return st;
+    if (M < 0 || activation < AWQ_ACT_NONE || activation > AWQ_ACT_GELU_TANH || (gated != 0 && gated != 1))
+        return AWQ_ERR_INVALID_ARG;
+    if (gated && (N & 1)) return AWQ_ERR_INVALID_ARG;
+    const int64_t n_out = gated ? N / 2 : N;
+    if (ldx < K || (ldx & 7) || ldy < n_out || (residual && ldr < n_out)) return AWQ_ERR_INVALID_ARG;
+    if (!qweight || !scales || (cfg.zero_point && !qzeros)) return AWQ_ERR_INVALID_ARG;
+    if (!empty && (!X || !Y)) return AWQ_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(qweight) || !aligned16(scales) || (cfg.zero_point && !aligned16(qzeros)))
+        return AWQ_ERR_INVALID_ARG;
+    const uintptr_t two = reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(residual) |
+                          reinterpret_cast<uintptr_t>(Y);
+    return (two & 1) ? AWQ_ERR_INVALID_ARG : AWQ_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uint32_t* qweight,
+                            const uint16_t* scales, const uint32_t* qzeros, int32_t N, int32_t K,
+                            awq_quant_config cfg, const uint16_t* bias, int32_t activation, int32_t gated,
+                            const uint16_t* residual, int64_t ldr, uint16_t* Y, int64_t ldy, void* stream) {
+    awq_status st = check_fused(X, M, ldx, qweight, scales, qzeros, N, K, cfg, bias, activation, gated, residual, ldr,
+                                Y, ldy, M == 0);
+    if (st != AWQ_OK) return st;
+    if (M == 0) return AWQ_OK;
+    const Epilogue ep = {bias, residual, (long long)ldr, Y, (long long)ldy, activation, gated};
+    return launch_linear_simple(X, M, ldx, nullptr, M, nullptr, 1, qweight, scales, cfg.zero_point ? qzeros : nullptr,
+                                N, K, cfg.q_group_size, ep, (cudaStream_t)stream);
+}
+
+awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const int32_t* rows, int32_t R,
+                              const int32_t* offsets, int32_t E, const uint32_t* qweight, const uint16_t* scales,
+                              const uint32_t* qzeros, int32_t N, int32_t K, awq_quant_config cfg,
+                              const uint16_t* bias, int32_t activation, int32_t gated, uint16_t* Y, int64_t ldy,
+                              void* stream) {
+    awq_status st = check_fused(X, T, ldx, qweight, scales, qzeros, N, K, cfg, bias, activation, gated, nullptr, 0, Y,
+                                ldy, R == 0 || T == 0);
+    if (st != AWQ_OK) return st;
+    if (R < 0 || E < 1 || E > kRouteMaxExperts || !offsets || !aligned4(offsets) || !aligned4(rows))
+        return AWQ_ERR_INVALID_ARG;
+    if ((int64_t)E * N > 0x7ffffe00LL) return AWQ_ERR_UNSUPPORTED;
+    if (R == 0) return AWQ_OK;
+    if (T == 0 || !Y || (!rows && T < R)) return AWQ_ERR_INVALID_ARG;
+    const Epilogue ep = {bias, nullptr, 0, Y, (long long)ldy, activation, gated};
+    return launch_linear_simple(X, T, ldx, rows, R, offsets, E, qweight, scales, cfg.zero_point ? qzeros : nullptr, N,
+                                K, cfg.q_group_size, ep, (cudaStream_t)stream);
+}
+
+size_t awq_moe_route_workspace_bytes(int32_t T, int32_t E) {
+    DeviceInfo d;
+    return route_workspace_bytes(T, E, device_info(d) ? d.sms : 148);
+}
+
+awq_status awq_moe_route(const void* logits, int32_t logits_fp16, int32_t T, int64_t ld, int32_t E, int32_t top_k,
+                         int32_t scoring, int32_t renormalize, float* weights, int32_t* experts, int32_t* offsets,
+                         int32_t* rows, int32_t* positions, void* ws, size_t ws_bytes, void* stream) {
+    if (T < 0 || E < 1 || top_k < 1 || top_k > E || ld < E) return AWQ_ERR_INVALID_ARG;
+    if ((logits_fp16 != 0 && logits_fp16 != 1) || (renormalize != 0 && renormalize != 1)) return AWQ_ERR_INVALID_ARG;
+    if (scoring != AWQ_SCORE_SOFTMAX && scoring != AWQ_SCORE_SIGMOID) return AWQ_ERR_INVALID_ARG;
+    if (E > kRouteMaxExperts || top_k > kRouteMaxTopK || T > (1 << 22)) return AWQ_ERR_UNSUPPORTED;
+    if (!offsets || (T && (!logits || !weights || !experts || !rows || !positions))) return AWQ_ERR_INVALID_ARG;
+    if (!aligned4(weights) || !aligned4(experts) || !aligned4(offsets) || !aligned4(rows) || !aligned4(positions) ||
+        !aligned16(ws) || (reinterpret_cast<uintptr_t>(logits) & (logits_fp16 ? 1u : 3u)))
+        return AWQ_ERR_INVALID_ARG;
+    DeviceInfo d;
+    if (!device_info(d)) return AWQ_ERR_CUDA;
+    if (ws_bytes < route_workspace_bytes(T, E, d.sms) || (!ws && route_workspace_bytes(T, E, d.sms)))
+        return AWQ_ERR_WORKSPACE;
+    RouteArgs a = {logits, (long long)ld, logits_fp16, T, E, top_k, scoring == AWQ_SCORE_SIGMOID, renormalize, weights,
+                   experts, offsets, rows, positions, static_cast<uint16_t*>(ws), 0, 1};
+    a.blocks = route_blocks(T, d.sms, a.per_block);
+    return launch_route(a, (cudaStream_t)stream);
+}
+
+awq_status awq_moe_combine(const uint16_t* Y, int32_t R, int64_t ldy, const float* weights, const int32_t* positions,
+                           int32_t T, int32_t top_k, int32_t N, const uint16_t* residual, int64_t ldr, uint16_t* out,
+                           int64_t ldo, void* stream) {
+    if (R < 0 || T < 0 || top_k < 1 || N < 1 || ldy < N || ldo < N || (residual && ldr < N)) return AWQ_ERR_INVALID_ARG;
+    if (ceil_div(N, kCombineThreads) > 65535) return AWQ_ERR_UNSUPPORTED;
+    if (T == 0) return AWQ_OK;
+    if ((R && !Y) || !weights || !positions || !out || !aligned4(weights) || !aligned4(positions))
+        return AWQ_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(Y) | reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(out)) & 1)
+        return AWQ_ERR_INVALID_ARG;
+    return launch_combine(Y, R, ldy, weights, positions, T, top_k, N, residual, ldr, out, ldo, (cudaStream_t)stream);
 }
 
 awq_status awq_check_bounded_wait(void* stream) {

@@ -222,6 +222,91 @@ awq_status awq_linear_gemm(const uint16_t* X, int32_t M, const uint32_t* qweight
                            awq_quant_config cfg, uint16_t* Y, void* ws, size_t ws_bytes,
                            void* stream);
 
+/* Activations of the fused linears' epilogue, all in fp32:
+ * SILU v / (1 + exp(-v)); GELU 0.5 v (1 + erf(v / sqrt 2));
+ * GELU_TANH 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))). */
+enum {
+    AWQ_ACT_NONE = 0,
+    AWQ_ACT_RELU = 1,
+    AWQ_ACT_SILU = 2,
+    AWQ_ACT_GELU = 3,
+    AWQ_ACT_GELU_TANH = 4
+};
+
+/*
+ * Dequantising linear with a fused epilogue, any M >= 0 (M = 0 does nothing).  With
+ * acc[m][n] = sum_k X[m][k] deq(W)[n][k] in fp32 (the linear entry points above):
+ *   gated = 0:  Y[m][n] = fp16( act(acc[m][n] + bias[n]) + residual[m][n] ),           n < N
+ *   gated = 1:  Y[m][f] = fp16( act(acc[m][f] + bias[f]) * (acc[m][F+f] + bias[F+f])
+ *                               + residual[m][f] ),  N = 2F, f < F
+ * (gated: the gate's rows of W stand before the other half's, as in a fused gate_up).
+ * bias [N] and residual [M][ldr] may be NULL.  residual may be Y itself (ldr = ldy); Y must
+ * not overlap any other input.  Rows may be strided: ldx, ldr, ldy are the distances of
+ * rows in elements; ldx a multiple of 8 (X 16-byte aligned as ever), while bias, residual
+ * and Y need only their element's alignment.  N need not be a multiple of anything.
+ * Needs no workspace.
+ */
+awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uint32_t* qweight,
+                            const uint16_t* scales, const uint32_t* qzeros, int32_t N, int32_t K,
+                            awq_quant_config cfg, const uint16_t* bias, int32_t activation, int32_t gated,
+                            const uint16_t* residual, int64_t ldr, uint16_t* Y, int64_t ldy, void* stream);
+
+/*
+ * The same linear grouped by expert: rows offsets[e] .. offsets[e+1]-1 of Y come from the
+ * weights of expert e (qweight [E][N][K/8], scales [E][N][K/G], qzeros [E][N][...],
+ * bias [E][N] or NULL), with the epilogue above without a residual.
+ *   Row p of Y reads row rows[p] of X [T][ldx], or row p where rows is NULL (then T >= R).
+ *   offsets [E+1] is a DEVICE table, 0 <= offsets[0] <= ... <= offsets[E] <= R; an expert
+ *   may have no row.  Rows of Y outside offsets[0] .. offsets[E]-1 are left as they were.
+ * The tables are read by the kernel, so the call neither synchronises nor depends on their
+ * values at capture.  Entries beyond the limits never read or write out of bounds: offsets
+ * are clamped to 0 .. R, and a row number outside 0 .. T-1 counts as a row of zeros.
+ * 1 <= E <= 1024, R >= 0 (0 does nothing).
+ */
+awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const int32_t* rows, int32_t R,
+                              const int32_t* offsets, int32_t E, const uint32_t* qweight,
+                              const uint16_t* scales, const uint32_t* qzeros, int32_t N, int32_t K,
+                              awq_quant_config cfg, const uint16_t* bias, int32_t activation, int32_t gated,
+                              uint16_t* Y, int64_t ldy, void* stream);
+
+/* Scores of awq_moe_route: softmax over all experts of a token, or sigmoid of each. */
+enum { AWQ_SCORE_SOFTMAX = 0, AWQ_SCORE_SIGMOID = 1 };
+
+/*
+ * Routing of T tokens to top_k of E experts, and the order of the chosen (token, slot) pairs by
+ * expert that awq_linear_grouped and awq_moe_combine read.  logits [T][ld], fp32 or (logits_fp16
+ * = 1) fp16.  Per token, slots j = 0 .. top_k-1 in falling order of the logit (ties: the lower
+ * expert first):
+ *   experts[t][j]    the expert, or -1 where only masked experts are left.  An expert is masked by
+ *                    a logit of -inf (or NaN); the lowest finite value is an ordinary logit.
+ *   weights[t][j]    fp32 softmax over the unmasked experts (sigmoid: of its logit), with
+ *                    renormalize = 1 divided by the sum over the token's slots; 0 for expert -1
+ *                    and where that sum is 0.  A logit of +inf counts as the largest finite fp32.
+ *   offsets [E+1]    rows offsets[e] .. offsets[e+1]-1 belong to expert e, in token order
+ *   rows [T top_k]   the token of each row, -1 behind the last expert's rows
+ *   positions[t][j]  the row of the slot, or -1 for expert -1
+ * 1 <= top_k <= min(E, 32), E <= 1024, 0 <= T <= 2^22 (T = 0 writes the offsets alone).  Needs
+ * ws_bytes >= awq_moe_route_workspace_bytes(T, E) (not to be used by two calls at once).
+ * Deterministic: the outputs depend on the logits alone.
+ */
+awq_status awq_moe_route(const void* logits, int32_t logits_fp16, int32_t T, int64_t ld, int32_t E,
+                         int32_t top_k, int32_t scoring, int32_t renormalize, float* weights,
+                         int32_t* experts, int32_t* offsets, int32_t* rows, int32_t* positions, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* Workspace bytes of awq_moe_route on the current device. */
+size_t awq_moe_route_workspace_bytes(int32_t T, int32_t E);
+
+/*
+ * Combination of a token's expert rows: out[t][n] = fp16( residual[t][n] +
+ * sum_j weights[t][j] Y[positions[t][j]][n] ), fp32 sums in slot order.  A position outside
+ * 0 .. R-1 contributes nothing (its weight is not read).  residual [T][ldr] may be NULL, and may
+ * be out itself.  Any T >= 0, top_k >= 1, N >= 1; rows may be strided, 2-byte aligned.
+ */
+awq_status awq_moe_combine(const uint16_t* Y, int32_t R, int64_t ldy, const float* weights,
+                           const int32_t* positions, int32_t T, int32_t top_k, int32_t N,
+                           const uint16_t* residual, int64_t ldr, uint16_t* out, int64_t ldo, void* stream);
+
 /*
  * awq_scale_search without a workspace argument, for callers that cannot allocate
  * device memory when they quantise (an allocator-less runtime, a memory pool that
