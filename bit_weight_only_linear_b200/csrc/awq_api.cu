@@ -16,7 +16,7 @@
 #include "gemm_sm100.cuh"
 #include "search.cuh"
 #include "clip.cuh"
-#include "linear_simple.cuh"
+#include "linear_tc.cuh"
 #include "moe.cuh"
 
 using namespace awq;
@@ -298,6 +298,12 @@ awq_status check_fused(const uint16_t* X, int M, int64_t ldx, const uint32_t* qw
     return (two & 1) ? AWQ_ERR_INVALID_ARG : AWQ_OK;
 }
 
+awq_status launch_linear(const LinearArgs& l, cudaStream_t st) {
+    DeviceInfo d;
+    if (!device_info(d)) return AWQ_ERR_CUDA;
+    return launch_linear_tc(l, d.sms, st);
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -313,8 +319,9 @@ awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uin
     if (st != AWQ_OK) return st;
     if (M == 0) return AWQ_OK;
     const Epilogue ep = {bias, residual, (long long)ldr, Y, (long long)ldy, activation, gated};
-    return launch_linear_simple(X, M, ldx, nullptr, M, nullptr, 1, qweight, scales, cfg.zero_point ? qzeros : nullptr,
-                                N, K, cfg.q_group_size, ep, (cudaStream_t)stream);
+    const LinearArgs l = {X, M, (long long)ldx, nullptr, M, nullptr, 1, qweight, scales,
+                          cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep};
+    return launch_linear(l, (cudaStream_t)stream);
 }
 
 awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const int32_t* rows, int32_t R,
@@ -331,8 +338,9 @@ awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const i
     if (R == 0) return AWQ_OK;
     if (T == 0 || !Y || (!rows && T < R)) return AWQ_ERR_INVALID_ARG;
     const Epilogue ep = {bias, nullptr, 0, Y, (long long)ldy, activation, gated};
-    return launch_linear_simple(X, T, ldx, rows, R, offsets, E, qweight, scales, cfg.zero_point ? qzeros : nullptr, N,
-                                K, cfg.q_group_size, ep, (cudaStream_t)stream);
+    const LinearArgs l = {X, T, (long long)ldx, rows, R, offsets, E, qweight, scales,
+                          cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep};
+    return launch_linear(l, (cudaStream_t)stream);
 }
 
 size_t awq_moe_route_workspace_bytes(int32_t T, int32_t E) {

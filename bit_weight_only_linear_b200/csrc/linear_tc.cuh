@@ -1,0 +1,611 @@
+// Fused linear and expert-grouped linear on the sm_100a tensor cores (tcgen05, TMA, TMEM),
+// with the dequantised weights as the TMEM operand.
+//
+// D[n][m] = sum_k deq(W)[n][k] X[m][k]: a tile is 256 weight rows (two MMA row tiles of 128) by
+// BN rows of X.  Gated, the two row tiles are 128 gate rows and the 128 rows F behind them, so
+// that both halves of an output sit in one TMEM lane and the epilogue needs no exchange.
+//
+//   * A from tensor memory: a dequantising thread is one weight row = one TMEM lane; it turns
+//     the row's packed codes into fp16 pairs and writes them with tcgen05.st.  Compared with an A
+//     tile in shared memory this takes the 128 x 64 fp16 write and the MMA's reads of it off
+//     shared memory, which at 128 B/cycle otherwise bounds the MMA: per 128 x BN x 16 MMA
+//     (BN / 2 cycles) the shared memory then carries B (BN / 4 cycles), half of the copy of X
+//     (BN / 8) and the packed words (16).
+//   * B = X in the 128-byte-swizzled K-major layout, by tiled TMA (rows in place) or by
+//     tile::gather4 (row numbers from a table: the experts' tokens), into a ring freed by the MMAs.
+//   * Packed weights: 256-code stages (a whole 128-byte line per row) in a ring of their own,
+//     freed by the dequantisers.
+//   * Few tiles: a cluster of `splits` CTAs shares the K of a tile; the fp32 partial sums meet in
+//     distributed shared memory and are added in rank order (no workspace, no second kernel).
+//   * Grouped: every expert's rows are cut into tiles of their own; a CTA finds its tile by a scan
+//     over the offsets table, so nothing is read back to the host.
+// Each dequantised weight is rounded once to fp16, as in awq_linear_gemm, whose range flag it
+// raises too.  Every wait is bounded: on time-out the kernel raises the device error word, drains
+// what it issued, frees TMEM and returns.
+#pragma once
+
+#include "common.cuh"
+#include "epilogue.cuh"
+#include "gemm_sm100.cuh"
+#include "launch.cuh"
+#include "sm100.cuh"
+
+namespace awq {
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 TMEM lanes x 16 consecutive 32-bit columns, from registers.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four rows of a 2-D tensor (box {64, 1}) into four consecutive 128-byte lines.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y0, int y1,
+                                            int y2, int y3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5, %6, %7}], [%2];" ::"r"(sm100::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(sm100::smem_u32(bar)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// fp32 at the shared-memory address `a` of this CTA, in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t a, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
+                 : "=f"(v)
+                 : "r"(a), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+constexpr int kTcRows = 256;             // weight rows per tile: two MMA row tiles
+constexpr int kTcWKB = 4;                // k-blocks (64 codes) per packed stage: 128-byte lines
+
+template <int BN>
+struct TcCfg {
+    // Up to 64 columns two CTAs share an SM (8 dequantising warps, half of TMEM each): one's
+    // start and epilogue overlap the other's stream.  Above, one CTA with 16 warps.
+    static constexpr int kCtas = BN <= 64 ? 2 : 1;
+    static constexpr int kDqWarps = BN <= 64 ? 8 : 16;
+    static constexpr int kThreads = 96 + 32 * kDqWarps;
+    static constexpr uint32_t kTmemCols = 512 / kCtas;
+    static constexpr int kABufs = BN <= 32 ? 3 : (BN == 128 ? 4 : 2);      // x 64 columns (two tiles x 64 codes)
+    static constexpr int kXStages = BN == 192 ? 5 : (BN == 128 ? 6 : (BN == 64 ? 5 : (BN == 32 ? 8 : 4)));
+    static constexpr int kWStages = BN == 64 || BN == 32 ? 2 : 3;
+    static constexpr int kXBytes = BN * 128;
+    static constexpr int kWBytes = kTcRows * 32 * kTcWKB;
+    static constexpr int kWOff = 0;
+    static constexpr int kXOff = kWOff + kWStages * kWBytes;
+    static constexpr int kRing = kXOff + kXStages * kXBytes;
+    static constexpr int kSrcOff = kRing;                                  // [BN] row numbers of X
+    static constexpr int kBarOff = kSrcOff + BN * 4;
+    static constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 2 * kABufs + 1;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;                // TMEM address, tile
+    static constexpr int kSmemBytes = kMiscOff + 32 + 1024;
+    static_assert(kSmemBytes <= (kCtas == 1 ? 232448 : 115712), "shared memory");
+    static_assert(2 * BN + kABufs * 64 <= (int)kTmemCols, "tensor memory");
+    static_assert(kTcRows * BN * 4 <= kRing, "the partial sums of a K split reuse the rings");
+};
+
+struct TcArgs {
+    const uint16_t* scales;
+    const uint32_t* qzeros;              // NULL: implicit zero 8
+    const int32_t* rows;                 // row numbers of X, or NULL
+    const int32_t* offsets;              // [E+1], or NULL: one range of R rows
+    int T, R, E, N, K, G;
+    int n_tiles;                         // tiles of weight rows
+    int m_tiles;                         // tiles of X rows (dense)
+    int kb_per;                          // k-blocks per split (a multiple of kTcWKB)
+    Epilogue ep;
+};
+
+// Row range of expert e, clamped into 0..R whatever the table holds.
+__device__ __forceinline__ int2 expert_range(const int32_t* offsets, int e, int R) {
+    const int b = min(max(__ldg(offsets + e), 0), R);
+    return make_int2(b, min(max(__ldg(offsets + e + 1), b), R));
+}
+
+// The `tile`-th row tile of the experts' ranges, each cut into tiles of `bn` rows: {expert, first
+// row, end of the expert's rows}, expert -1 if there are fewer tiles.  By a whole warp.  `per`
+// consecutive tile numbers belong to each row tile (its tiles of weight rows); the caller gets the
+// remainder in `sub`, with the row tiles of an expert innermost.
+__device__ __forceinline__ int4 find_tile(const int32_t* offsets, int E, int R, int bn, int per, long long tile) {
+    const int lane = threadIdx.x & 31;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        int2 g = make_int2(0, 0);
+        if (e < E) g = expert_range(offsets, e, R);
+        const int mt = (g.y - g.x + bn - 1) / bn;
+        long long x = (long long)mt * per, v = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        const long long total = __shfl_sync(0xffffffffu, x, 31);
+        if (tile < total) {
+            const bool mine = tile >= x - v && tile < x;
+            const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+            const int in = (int)(tile - (x - v));          // tile inside the expert
+            const int m = mt ? in % mt : 0, n = mt ? in / mt : 0;
+            int4 r = make_int4(e, g.x + m * bn, g.y, n);
+            r.x = __shfl_sync(0xffffffffu, r.x, src);
+            r.y = __shfl_sync(0xffffffffu, r.y, src);
+            r.z = __shfl_sync(0xffffffffu, r.z, src);
+            r.w = __shfl_sync(0xffffffffu, r.w, src);
+            return r;
+        }
+        tile -= total;
+    }
+    return make_int4(-1, 0, 0, 0);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(TcCfg<BN>::kThreads, TcCfg<BN>::kCtas)
+linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_q,
+                 const TcArgs a) {
+    using C = TcCfg<BN>;
+    using namespace sm100;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+    uint64_t* xfull = bars;                         // [kXStages] X landed
+    uint64_t* xempty = xfull + C::kXStages;         // [kXStages] MMAs done with the slot
+    uint64_t* wfull = xempty + C::kXStages;         // [kWStages] packed stage landed
+    uint64_t* wempty = wfull + C::kWStages;         // [kWStages] dequantisers have read it
+    uint64_t* afull = wempty + C::kWStages;         // [kABufs]   dequantised k-block in TMEM
+    uint64_t* aempty = afull + C::kABufs;           // [kABufs]   MMAs done with it
+    uint64_t* tfull = aempty + C::kABufs;           // accumulators complete
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    int32_t* src = reinterpret_cast<int32_t*>(smem + C::kSrcOff);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    uint32_t splits;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+    const uint32_t rank = cluster_rank();
+    const int tile = blockIdx.x / splits;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kXStages; ++s) {
+            mbar_init(&xfull[s], 1);
+            mbar_init(&xempty[s], 1);
+        }
+        for (int s = 0; s < C::kWStages; ++s) {
+            mbar_init(&wfull[s], 1);
+            mbar_init(&wempty[s], C::kDqWarps);
+        }
+        for (int b = 0; b < C::kABufs; ++b) {
+            mbar_init(&afull[b], C::kDqWarps);
+            mbar_init(&aempty[b], 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_fence_init();
+        prefetch_tensormap(&tmap_x);
+        prefetch_tensormap(&tmap_q);
+    }
+    if (warp == 1) {
+        tmem_alloc(&misc[0], C::kTmemCols);
+        tmem_relinquish();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {
+        // the CTA's tile and the rows of X that it reads
+        int4 t;
+        if (a.offsets)
+            t = find_tile(a.offsets, a.E, a.R, BN, a.n_tiles, tile);
+        else
+            t = make_int4(0, (tile % a.m_tiles) * BN, a.R, tile / a.m_tiles);
+        if (lane == 0) {
+            misc[1] = (uint32_t)t.x;
+            misc[2] = (uint32_t)t.y;
+            misc[3] = (uint32_t)t.z;
+            misc[4] = (uint32_t)t.w;
+        }
+        if (t.x >= 0)
+            for (int c = lane; c < BN; c += 32) {
+                const int p = t.y + c;
+                int s = -1;
+                if (p < t.z) {
+                    s = a.rows ? __ldg(a.rows + p) : p;
+                    if (s < 0 || s >= a.T) s = -1;
+                }
+                src[c] = s;
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const int expert = (int)misc[1], r0 = (int)misc[2], r1 = (int)misc[3], nt = (int)misc[4];
+    const int F = a.ep.gated ? a.N / 2 : a.N;
+    // weight rows of the two row tiles inside the expert, and where they end
+    const int n0 = a.ep.gated ? nt * 128 : nt * kTcRows;
+    const int n1 = a.ep.gated ? F + n0 : n0 + 128;
+    const int end0 = F, end1 = a.N;
+    const int kb0 = rank * a.kb_per;
+    const int num_kb = expert < 0 ? 0 : max(0, min(a.kb_per, ceil_div(a.K, kGemmKB) - kb0));
+    const uint32_t acc0 = tmem, abase = tmem + 2 * BN;
+
+    if (warp == 0) {
+        // ---------------- X ring ----------------
+        int issued = 0;
+        bool ok = true;
+        for (int j = 0; j < num_kb; ++j) {
+            const int s = j % C::kXStages;
+            if (j >= C::kXStages) ok = mbar_wait(&xempty[s], ((j / C::kXStages) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            uint8_t* dst = smem + C::kXOff + s * C::kXBytes;
+            if (lane == 0) mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
+            __syncwarp();
+            if (a.rows) {
+                // rows that do not exist are read from row 0; their columns are never stored
+                // (or are stored as those of a row of zeros)
+                for (int c = lane; c < BN / 4; c += 32) {
+                    const int4 r = *reinterpret_cast<const int4*>(src + 4 * c);
+                    tma_gather4(dst + c * 512, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, max(r.x, 0), max(r.y, 0),
+                                max(r.z, 0), max(r.w, 0));
+                }
+            } else if (lane == 0) {
+                tma_load_2d(dst, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, r0);
+            }
+            ++issued;
+        }
+        // every issued copy must land before the CTA may exit (or its ring be reused)
+        for (int j = issued - 1; j >= 0 && j >= issued - C::kXStages; --j)
+            mbar_wait(&xfull[j % C::kXStages], (j / C::kXStages) & 1);
+    } else if (warp == 2) {
+        if (lane == 0) {
+            // ---------------- packed-weight ring ----------------
+            const int n_st = ceil_div(num_kb, kTcWKB);
+            int issued = 0;
+            for (int j = 0; j < n_st; ++j) {
+                const int s = j % C::kWStages;
+                if (j >= C::kWStages && !mbar_wait(&wempty[s], ((j / C::kWStages) - 1) & 1)) break;
+                uint8_t* dst = smem + C::kWOff + s * C::kWBytes;
+                const int x = (kb0 + j * kTcWKB) * (kGemmKB / 8);
+                mbar_arrive_expect_tx(&wfull[s], C::kWBytes);
+                tma_load_2d(dst, &tmap_q, &wfull[s], x, expert * a.N + n0);
+                tma_load_2d(dst + C::kWBytes / 2, &tmap_q, &wfull[s], x, expert * a.N + n1);
+                ++issued;
+            }
+            for (int j = issued - 1; j >= 0 && j >= issued - C::kWStages; --j)
+                mbar_wait(&wfull[j % C::kWStages], (j / C::kWStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer ----------------
+            constexpr uint32_t idesc = idesc_f16_f32(128, BN);
+            bool ok = true;
+            for (int kb = 0; kb < num_kb; ++kb) {
+                const int s = kb % C::kXStages;
+                const int b = kb % C::kABufs;
+                ok = mbar_wait(&xfull[s], (kb / C::kXStages) & 1) && mbar_wait(&afull[b], (kb / C::kABufs) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t bdesc = desc_sw128_kmajor(smem_u32(smem + C::kXOff + s * C::kXBytes));
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int kk = 0; kk < kGemmKB / 16; ++kk)
+                        mma_f16_ts(acc0 + h * BN, abase + (b * 2 + h) * 32 + kk * 8, bdesc + 2 * kk, idesc,
+                                   (kb | kk) != 0);
+                mma_commit(&xempty[s]);
+                mma_commit(&aempty[b]);
+            }
+            mma_commit(tfull);   // also on the error path, so that the MMAs drain before TMEM is freed
+            mbar_wait(tfull, 0);
+        }
+    } else {
+        // ---------------- dequantise: thread = weight row = TMEM lane ----------------
+        constexpr int kSets = C::kDqWarps / 4;
+        constexpr int kParts = 4 / kSets;         // 32-code halves of a k-block per thread: 1 or 2
+        const int q = warp & 3;                   // TMEM lane quarter of this warp
+        const int set = (warp - 3) >> 2;
+        const int h = set & 1;                    // row tile
+        const int part0 = kParts == 1 ? set >> 1 : 0;
+        const int r = q * 32 + lane;
+        const int n = (h ? n1 : n0) + r;
+        const bool row_ok = n < (h ? end1 : end0);
+        const int ng = a.K / a.G;
+        const int nzw = ceil_div(ng, 8);
+        const bool zp = a.qzeros != nullptr;
+        const int lg = 31 - __clz(a.G);           // G is a power of two
+        const size_t wrow = (size_t)max(expert, 0) * a.N + (row_ok ? n : 0);
+        const uint16_t* srow = a.scales + wrow * ng;
+        const uint32_t* zrow = a.qzeros + wrow * nzw;
+        // the next group's scale and zero word are fetched a group ahead of their use
+        const int k_first = kb0 * kGemmKB + part0 * 32;
+        const int step = (kParts == 1 ? kGemmKB : 32) >> lg;      // groups between a thread's 32-code parts
+        uint32_t sc_next = 0, zw_next = 0;
+        if (k_first < a.K && num_kb > 0) {
+            sc_next = __ldg(srow + (k_first >> lg));
+            if (zp) zw_next = __ldg(zrow + (k_first >> (lg + 3)));
+        }
+        int g_cur = -1;
+        uint32_t s2 = 0, zmagic = 0x64006400u, zneg16 = 0;
+        bool ok = true;
+        for (int kb = 0; kb < num_kb; ++kb) {
+            const int j = kb / kTcWKB, sb = kb % kTcWKB;
+            const int b = kb % C::kABufs;
+            if (sb == 0) ok = mbar_wait(&wfull[j % C::kWStages], (j / C::kWStages) & 1);
+            uint4 packed[kParts];
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+                packed[i] = *reinterpret_cast<const uint4*>(
+                    smem + C::kWOff + (j % C::kWStages) * C::kWBytes + h * (C::kWBytes / 2) +
+                    wstage_swizzle<kTcWKB>((uint32_t)(r * 128 + sb * 32 + (part0 + i) * 16)));
+            if (ok && kb >= C::kABufs) ok = mbar_wait(&aempty[b], ((kb / C::kABufs) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const int k = (kb0 + kb) * kGemmKB + (part0 + i) * 32;
+                const int g = k >> lg;
+                if (g != g_cur && k < a.K) {       // (codes past K are zeros times X's zeros)
+                    g_cur = g;
+                    const uint32_t sc = sc_next;
+                    const uint32_t z = zp ? ((zw_next >> (4 * (g & 7))) & 15u) : 8u;
+                    s2 = sc | (sc << 16);
+                    const uint32_t zm = 0x6400u | z;                        // 1024 + z
+                    zmagic = zm | (zm << 16);
+                    const uint32_t zn = 0xD000u | (z << 4) | 0x0400u;       // -(64 + z)
+                    zneg16 = zn | (zn << 16);
+                    const float qz_max = zp ? fmaxf((float)z, 15.0f - (float)z) : 8.0f;
+                    const float sf = h2f((uint16_t)sc);
+                    if (row_ok && !(sf * qz_max < 65520.0f) && !isnan(sf)) raise_error(kErrRange);
+                    const int gn = g + max(1, step);
+                    if (((long long)gn << lg) < a.K) {
+                        sc_next = __ldg(srow + gn);
+                        if (zp) zw_next = __ldg(zrow + (gn >> 3));
+                    }
+                }
+                uint32_t v[16];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t word = w == 0 ? packed[i].x : (w == 1 ? packed[i].y : (w == 2 ? packed[i].z : packed[i].w));
+                    const uint4 d = dequant_word(word, zmagic, zneg16, s2);
+                    v[4 * w] = d.x, v[4 * w + 1] = d.y, v[4 * w + 2] = d.z, v[4 * w + 3] = d.w;
+                }
+                tmem_st16(abase + ((uint32_t)(q * 32) << 16) + (uint32_t)((b * 2 + h) * 32 + (part0 + i) * 16), v);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (sb == kTcWKB - 1 || kb == num_kb - 1) mbar_arrive(&wempty[j % C::kWStages]);
+                mbar_arrive(&afull[b]);
+            }
+        }
+        ok = ok && num_kb > 0 && mbar_wait(tfull, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+
+        // ---------------- epilogue ----------------
+        const Epilogue& ep = a.ep;
+        const uint16_t* bias = ep.bias ? ep.bias + (size_t)max(expert, 0) * a.N : nullptr;
+        if (splits == 1) {
+            if (ok) {
+                // gated: a warp takes both accumulators of its lanes and 1/kSets of the columns;
+                // else one accumulator and 2/kSets of the columns
+                const int hh = set & 1;
+                const int cw = ep.gated ? BN / kSets : BN * 2 / kSets;
+                const int c0 = ep.gated ? set * cw : (set >> 1) * cw;
+                const int nn = (ep.gated ? n0 : (hh ? n1 : n0)) + r;
+                const bool out_ok = nn < (ep.gated ? F : a.N);
+                const float b0 = bias && out_ok ? h2f(bias[nn]) : 0.0f;
+                const float b1 = bias && out_ok && ep.gated ? h2f(bias[F + nn]) : 0.0f;
+                constexpr int CH = BN / kSets < 16 ? 8 : 16;          // columns at a time
+                const uint32_t lanes = (uint32_t)(q * 32) << 16;
+                for (int c = c0; c < c0 + cw; c += CH) {
+                    if (r0 + c >= r1) break;
+                    uint32_t u0[CH], u1[CH];
+                    const uint32_t a0 = acc0 + (ep.gated ? 0 : hh * BN) + lanes + (uint32_t)c;
+                    if constexpr (CH == 16) {
+                        tmem_ld16(a0, u0);
+                        if (ep.gated) tmem_ld16(a0 + BN, u1);
+                    } else {
+                        tmem_ld8(a0, u0);
+                        if (ep.gated) tmem_ld8(a0 + BN, u1);
+                    }
+                    float res[CH];
+#pragma unroll
+                    for (int i = 0; i < CH; ++i)
+                        res[i] = ep.residual && out_ok && r0 + c + i < r1
+                                     ? h2f(ep.residual[(size_t)(r0 + c + i) * ep.ldr + nn])
+                                     : 0.0f;
+                    tmem_ld_wait();
+                    if (out_ok) {
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            const int m = r0 + c + i;
+                            if (m >= r1) break;
+                            const bool live = !a.rows || src[c + i] >= 0;
+                            float y = apply_act((live ? __uint_as_float(u0[i]) : 0.0f) + b0, ep.act);
+                            if (ep.gated) y *= (live ? __uint_as_float(u1[i]) : 0.0f) + b1;
+                            ep.Y[(size_t)m * ep.ldy + nn] = f2h_rn(y + res[i]);
+                        }
+                    }
+                }
+            }
+        } else if (ok) {
+            // partial sums into this CTA's shared memory: [column][256 rows]
+            float* part = reinterpret_cast<float*>(smem);
+            const uint32_t lanes = (uint32_t)(q * 32) << 16;
+            constexpr int cw = BN * 2 / kSets;
+            constexpr int CH = cw < 16 ? 8 : 16;
+            const int c0 = (set >> 1) * cw;
+            for (int c = c0; c < c0 + cw; c += CH) {
+                uint32_t u[CH];
+                if constexpr (CH == 16) tmem_ld16(acc0 + h * BN + lanes + (uint32_t)c, u);
+                else tmem_ld8(acc0 + h * BN + lanes + (uint32_t)c, u);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < CH; ++i) part[(c + i) * kTcRows + h * 128 + r] = __uint_as_float(u[i]);
+            }
+        } else {
+            float* part = reinterpret_cast<float*>(smem);
+            // no k-block of this split (or a time-out, which is flagged): it adds nothing
+            for (int i = threadIdx.x - 96; i < kTcRows * BN; i += 32 * C::kDqWarps) part[i] = 0.0f;
+        }
+    }
+    if (splits > 1) {
+        __syncwarp();
+        cluster_sync_all();
+        // rank's share of the outputs: columns rank, rank + splits, ..; the partial sums in rank order
+        const float* part = reinterpret_cast<const float*>(smem);
+        const uint32_t base = smem_u32(part);
+        const Epilogue& ep = a.ep;
+        const int per_col = ep.gated ? 128 : kTcRows;
+        const int cols = expert < 0 ? 0 : min(BN, r1 - r0);
+        const int mine = cols > (int)rank ? (cols - 1 - (int)rank) / (int)splits + 1 : 0;
+        const uint16_t* bias = ep.bias ? ep.bias + (size_t)max(expert, 0) * a.N : nullptr;
+        for (int i = threadIdx.x; i < mine * per_col; i += C::kThreads) {
+            const int c = (int)rank + (i / per_col) * (int)splits, l = i % per_col;
+            const int nn = n0 + l;                 // (not gated: n1 = n0 + 128)
+            if (nn >= F) continue;
+            const int m = r0 + c;
+            const uint32_t at = base + (uint32_t)(c * kTcRows + l) * 4;
+            float v0 = 0.0f, v1 = 0.0f;
+            for (uint32_t s = 0; s < splits; ++s) {
+                v0 += ld_cluster(at, s);
+                if (ep.gated) v1 += ld_cluster(at + 512, s);
+            }
+            if (a.rows && src[c] < 0) v0 = v1 = 0.0f;
+            float y = apply_act(v0 + (bias ? h2f(bias[nn]) : 0.0f), ep.act);
+            if (ep.gated) y *= v1 + (bias ? h2f(bias[F + nn]) : 0.0f);
+            if (ep.residual) y += h2f(ep.residual[(size_t)m * ep.ldr + nn]);
+            ep.Y[(size_t)m * ep.ldy + nn] = f2h_rn(y);
+        }
+        __syncwarp();
+        cluster_sync_all();     // no CTA leaves while another reads its shared memory
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+struct LinearArgs {
+    const uint16_t* X;
+    int T;                       // rows of X
+    long long ldx;
+    const int32_t* rows;         // row numbers of X per output row, or NULL
+    int R;                       // output rows
+    const int32_t* offsets;      // [E+1] or NULL (dense: one range of R rows)
+    int E;
+    const uint32_t* qweight;
+    const uint16_t* scales;
+    const uint32_t* qzeros;      // NULL: implicit zero 8
+    int N, K, G;
+    Epilogue ep;
+};
+
+inline bool make_tmap_ld(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t rows, uint64_t cols,
+                         uint64_t row_bytes, uint32_t box_rows, uint32_t box_cols) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
+    using C = TcCfg<BN>;
+    CUtensorMap tx, tq;
+    if (!make_tmap_ld(&tx, l.X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)l.T, (uint64_t)l.K, (uint64_t)l.ldx * 2,
+                      l.rows ? 1 : BN, kGemmKB))
+        return AWQ_ERR_CUDA;
+    if (!make_tmap_ld(&tq, l.qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, (uint64_t)l.E * l.N, (uint64_t)(l.K / 8),
+                      (uint64_t)l.K / 2, 128, kTcWKB * kGemmKB / 8))
+        return AWQ_ERR_CUDA;
+    const void* fn = (const void*)linear_tc_kernel<BN>;
+    if (!prepare_kernel(fn)) return AWQ_ERR_CUDA;
+    TcArgs a = {l.scales, l.qzeros, l.rows, l.offsets, l.T, l.R, l.E, l.N, l.K, l.G, 0, 0, 0, l.ep};
+    a.n_tiles = l.ep.gated ? ceil_div(l.N / 2, 128) : ceil_div(l.N, kTcRows);
+    a.m_tiles = ceil_div(l.R, BN);
+    const int num_kb = ceil_div(l.K, kGemmKB);
+    a.kb_per = ceil_div(ceil_div(num_kb, splits), kTcWKB) * kTcWKB;
+    // grouped: the experts that have rows add at most one partial tile each
+    const long long mt = l.offsets ? (long long)l.R / BN + std::min(l.R, l.E) : a.m_tiles;
+    const long long ctas = mt * a.n_tiles * splits;
+    if (ctas > 0x7fffffffLL) return AWQ_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)ctas);
+    lc.blockDim = dim3(C::kThreads);
+    lc.dynamicSmemBytes = C::kSmemBytes;
+    lc.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    void* args[] = {&tx, &tq, &a};
+    return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+// K splits (CTAs of a cluster) for `tiles` tiles on `slots` CTA slots: doubled while the tiles leave
+// at least half of the slots idle and a split keeps two packed stages (512 codes).
+inline int tc_splits(long long tiles, int slots, int K) {
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= slots && ceil_div(K, kGemmKB * kTcWKB) >= 4 * s) s *= 2;
+    return s;
+}
+
+inline awq_status launch_linear_tc(const LinearArgs& l, int sms, cudaStream_t st) {
+    // rows per tile: the dense batch, or the experts' average share of the rows
+    const int active = l.offsets ? std::min(l.R, l.E) : 1;
+    const int share = ceil_div(l.R, active);
+    const int bn = share <= 16 ? 16 : share <= 32 ? 32 : share <= 64 ? 64 : share <= 128 ? 128 : 192;
+    const int n_tiles = l.ep.gated ? ceil_div(l.N / 2, 128) : ceil_div(l.N, kTcRows);
+    const long long tiles = (long long)active * ceil_div(share, bn) * n_tiles;
+    const int splits = tc_splits(tiles, sms * (bn <= 64 ? 2 : 1), l.K);
+    switch (bn) {
+        case 16: return launch_tc_bn<16>(l, splits, st);
+        case 32: return launch_tc_bn<32>(l, splits, st);
+        case 64: return launch_tc_bn<64>(l, splits, st);
+        case 128: return launch_tc_bn<128>(l, splits, st);
+        default: return launch_tc_bn<192>(l, splits, st);
+    }
+}
+
+}  // namespace awq

@@ -244,7 +244,7 @@ enum {
  * not overlap any other input.  Rows may be strided: ldx, ldr, ldy are the distances of
  * rows in elements; ldx a multiple of 8 (X 16-byte aligned as ever), while bias, residual
  * and Y need only their element's alignment.  N need not be a multiple of anything.
- * Needs no workspace.
+ * Needs no workspace.  Range: as awq_linear_gemm when M > 8 (AWQ_ERR_RANGE).
  */
 awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uint32_t* qweight,
                             const uint16_t* scales, const uint32_t* qzeros, int32_t N, int32_t K,

@@ -118,6 +118,18 @@ def test_linear_fused_overflow_to_inf(lib):
     assert torch.isinf(y).all() and (y > 0).all()
 
 
+def test_linear_fused_range_flag(lib):
+    """Weights beyond fp16 are flagged, as in linear_gemm."""
+    N, K, G = 64, 128, 128
+    q, s, z = R.packed(40, N, K, G, True)
+    X = torch.full((16, K), 60000.0, dtype=torch.float16, device="cuda")
+    lib.linear_fused(X, torch.full_like(q, -1), torch.full_like(s, 60000.0), torch.zeros_like(z), G, True)
+    with pytest.raises(lib.AWQError) as e:
+        lib.device_error()
+    assert e.value.status == lib.AWQ_ERR_RANGE
+    lib.device_error()
+
+
 def test_linear_fused_agrees_with_linear_gemm(lib):
     """Without an epilogue it is the linear of the other entry points (fp32 sums in another order)."""
     w = R.packed(45, 512, 1024, 128, True)
