@@ -27,6 +27,7 @@
 #include "common.cuh"
 #include "epilogue.cuh"
 #include "gemm_sm100.cuh"
+#include "gemv.cuh"
 #include "launch.cuh"
 #include "sm100.cuh"
 
@@ -91,7 +92,11 @@ struct TcCfg {
     // start and epilogue overlap the other's stream.  Above, one CTA with 16 warps.
     static constexpr int kCtas = BN <= 64 ? 2 : 1;
     static constexpr int kDqWarps = BN <= 64 ? 8 : 16;
-    static constexpr int kThreads = 96 + 32 * kDqWarps;
+    // Warps that issue the copies of X: a gathered k-block takes BN / 4 copy instructions, a tiled one
+    // takes one.
+    static constexpr int kXWarps = BN >= 64 ? 4 : (BN == 32 ? 2 : 1);
+    static constexpr int kMmaWarp = kXWarps, kWWarp = kXWarps + 1, kDqWarp0 = kXWarps + 2;
+    static constexpr int kThreads = 32 * (kDqWarp0 + kDqWarps);
     static constexpr uint32_t kTmemCols = 512 / kCtas;
     static constexpr int kABufs = BN <= 32 ? 3 : (BN == 128 ? 4 : 2);      // x 64 columns (two tiles x 64 codes)
     static constexpr int kXStages = BN == 192 ? 5 : (BN == 128 ? 6 : (BN == 64 ? 5 : (BN == 32 ? 8 : 4)));
@@ -208,7 +213,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         prefetch_tensormap(&tmap_x);
         prefetch_tensormap(&tmap_q);
     }
-    if (warp == 1) {
+    if (warp == C::kMmaWarp) {
         tmem_alloc(&misc[0], C::kTmemCols);
         tmem_relinquish();
     }
@@ -252,71 +257,73 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     const int num_kb = expert < 0 ? 0 : max(0, min(a.kb_per, ceil_div(a.K, kGemmKB) - kb0));
     const uint32_t acc0 = tmem, abase = tmem + 2 * BN;
 
-    if (warp == 0) {
+    if (warp < C::kXWarps) {
         // ---------------- X ring ----------------
-        int issued = 0;
-        bool ok = true;
-        for (int j = 0; j < num_kb; ++j) {
-            const int s = j % C::kXStages;
-            if (j >= C::kXStages) ok = mbar_wait(&xempty[s], ((j / C::kXStages) - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            uint8_t* dst = smem + C::kXOff + s * C::kXBytes;
-            if (lane == 0) mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
-            __syncwarp();
-            if (a.rows) {
-                // rows that do not exist are read from row 0; their columns are never stored
-                // (or are stored as those of a row of zeros)
-                for (int c = lane; c < BN / 4; c += 32) {
-                    const int4 r = *reinterpret_cast<const int4*>(src + 4 * c);
-                    tma_gather4(dst + c * 512, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, max(r.x, 0), max(r.y, 0),
-                                max(r.z, 0), max(r.w, 0));
+        if ((a.rows || warp == 0) && elect_one()) {
+            int issued = 0, s = 0;
+            uint32_t ph = 0;
+            for (int j = 0; j < num_kb; ++j) {
+                if (!mbar_wait(&xempty[s], ph ^ 1u)) break;
+                uint8_t* dst = smem + C::kXOff + s * C::kXBytes;
+                if (warp == 0) mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
+                if (a.rows) {
+                    // rows that do not exist are read from row 0; their columns are never stored
+                    // (or are stored as those of a row of zeros)
+                    for (int c = warp; c < BN / 4; c += C::kXWarps) {
+                        const int4 r = *reinterpret_cast<const int4*>(src + 4 * c);
+                        tma_gather4(dst + c * 512, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, max(r.x, 0), max(r.y, 0),
+                                    max(r.z, 0), max(r.w, 0));
+                    }
+                } else {
+                    tma_load_2d(dst, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, r0);
                 }
-            } else if (lane == 0) {
-                tma_load_2d(dst, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, r0);
+                ++issued;
+                if (++s == C::kXStages) s = 0, ph ^= 1u;
             }
-            ++issued;
+            // every issued copy must land before the CTA may exit (or its ring be reused)
+            for (int j = issued - 1; j >= 0 && j >= issued - C::kXStages; --j)
+                mbar_wait(&xfull[j % C::kXStages], (j / C::kXStages) & 1);
         }
-        // every issued copy must land before the CTA may exit (or its ring be reused)
-        for (int j = issued - 1; j >= 0 && j >= issued - C::kXStages; --j)
-            mbar_wait(&xfull[j % C::kXStages], (j / C::kXStages) & 1);
-    } else if (warp == 2) {
-        if (lane == 0) {
+    } else if (warp == C::kWWarp) {
+        if (elect_one()) {
             // ---------------- packed-weight ring ----------------
             const int n_st = ceil_div(num_kb, kTcWKB);
-            int issued = 0;
+            int issued = 0, s = 0;
+            uint32_t ph = 0;
             for (int j = 0; j < n_st; ++j) {
-                const int s = j % C::kWStages;
-                if (j >= C::kWStages && !mbar_wait(&wempty[s], ((j / C::kWStages) - 1) & 1)) break;
+                if (!mbar_wait(&wempty[s], ph ^ 1u)) break;
                 uint8_t* dst = smem + C::kWOff + s * C::kWBytes;
                 const int x = (kb0 + j * kTcWKB) * (kGemmKB / 8);
                 mbar_arrive_expect_tx(&wfull[s], C::kWBytes);
                 tma_load_2d(dst, &tmap_q, &wfull[s], x, expert * a.N + n0);
                 tma_load_2d(dst + C::kWBytes / 2, &tmap_q, &wfull[s], x, expert * a.N + n1);
                 ++issued;
+                if (++s == C::kWStages) s = 0, ph ^= 1u;
             }
             for (int j = issued - 1; j >= 0 && j >= issued - C::kWStages; --j)
                 mbar_wait(&wfull[j % C::kWStages], (j / C::kWStages) & 1);
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
+    } else if (warp == C::kMmaWarp) {
+        if (elect_one()) {
             // ---------------- MMA issuer ----------------
             constexpr uint32_t idesc = idesc_f16_f32(128, BN);
-            bool ok = true;
+            const uint64_t bdesc0 = desc_sw128_kmajor(smem_u32(smem + C::kXOff));
+            int s = 0, b = 0;
+            uint32_t xph = 0, aph = 0;
             for (int kb = 0; kb < num_kb; ++kb) {
-                const int s = kb % C::kXStages;
-                const int b = kb % C::kABufs;
-                ok = mbar_wait(&xfull[s], (kb / C::kXStages) & 1) && mbar_wait(&afull[b], (kb / C::kABufs) & 1);
-                if (!ok) break;
+                if (!mbar_wait(&xfull[s], xph) || !mbar_wait(&afull[b], aph)) break;
                 tc_fence_after();
-                const uint64_t bdesc = desc_sw128_kmajor(smem_u32(smem + C::kXOff + s * C::kXBytes));
+                const uint64_t bdesc = bdesc0 + (uint64_t)(s * (C::kXBytes >> 4));
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int kk = 0; kk < kGemmKB / 16; ++kk)
                         mma_f16_ts(acc0 + h * BN, abase + (b * 2 + h) * 32 + kk * 8, bdesc + 2 * kk, idesc,
                                    (kb | kk) != 0);
-                mma_commit(&xempty[s]);
                 mma_commit(&aempty[b]);
+                mma_commit(&xempty[s]);
+                if (++s == C::kXStages) s = 0, xph ^= 1u;
+                if (++b == C::kABufs) b = 0, aph ^= 1u;
             }
             mma_commit(tfull);   // also on the error path, so that the MMAs drain before TMEM is freed
             mbar_wait(tfull, 0);
@@ -326,7 +333,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         constexpr int kSets = C::kDqWarps / 4;
         constexpr int kParts = 4 / kSets;         // 32-code halves of a k-block per thread: 1 or 2
         const int q = warp & 3;                   // TMEM lane quarter of this warp
-        const int set = (warp - 3) >> 2;
+        const int set = (warp - C::kDqWarp0) >> 2;
         const int h = set & 1;                    // row tile
         const int part0 = kParts == 1 ? set >> 1 : 0;
         const int r = q * 32 + lane;
@@ -340,67 +347,73 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         const uint16_t* srow = a.scales + wrow * ng;
         const uint32_t* zrow = a.qzeros + wrow * nzw;
         // the next group's scale and zero word are fetched a group ahead of their use
-        const int k_first = kb0 * kGemmKB + part0 * 32;
-        const int step = (kParts == 1 ? kGemmKB : 32) >> lg;      // groups between a thread's 32-code parts
+        int k = kb0 * kGemmKB + part0 * 32;
+        const int gstep = max(1, (kParts == 1 ? kGemmKB : 32) >> lg);   // groups between a thread's parts
         uint32_t sc_next = 0, zw_next = 0;
-        if (k_first < a.K && num_kb > 0) {
-            sc_next = __ldg(srow + (k_first >> lg));
-            if (zp) zw_next = __ldg(zrow + (k_first >> (lg + 3)));
+        if (k < a.K && num_kb > 0) {
+            sc_next = __ldg(srow + (k >> lg));
+            if (zp) zw_next = __ldg(zrow + (k >> (lg + 3)));
         }
         int g_cur = -1;
         uint32_t s2 = 0, zmagic = 0x64006400u, zneg16 = 0;
+        const uint32_t wline = smem_u32(smem + C::kWOff) + (uint32_t)(h * (C::kWBytes / 2) + r * 128);
+        const uint32_t aline = abase + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 32 + part0 * 16);
         bool ok = true;
-        for (int kb = 0; kb < num_kb; ++kb) {
-            const int j = kb / kTcWKB, sb = kb % kTcWKB;
-            const int b = kb % C::kABufs;
-            if (sb == 0) ok = mbar_wait(&wfull[j % C::kWStages], (j / C::kWStages) & 1);
-            uint4 packed[kParts];
+        int ws = 0, b = 0;
+        uint32_t wph = 0, aph = 0;
+        for (int kb = 0; kb < num_kb && ok; kb += kTcWKB) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&wfull[ws], wph));
+            if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < kParts; ++i)
-                packed[i] = *reinterpret_cast<const uint4*>(
-                    smem + C::kWOff + (j % C::kWStages) * C::kWBytes + h * (C::kWBytes / 2) +
-                    wstage_swizzle<kTcWKB>((uint32_t)(r * 128 + sb * 32 + (part0 + i) * 16)));
-            if (ok && kb >= C::kABufs) ok = mbar_wait(&aempty[b], ((kb / C::kABufs) - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            tc_fence_after();
+            for (int sb = 0; sb < kTcWKB; ++sb) {
+                if (kb + sb >= num_kb) break;
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-                const int k = (kb0 + kb) * kGemmKB + (part0 + i) * 32;
-                const int g = k >> lg;
-                if (g != g_cur && k < a.K) {       // (codes past K are zeros times X's zeros)
-                    g_cur = g;
-                    const uint32_t sc = sc_next;
-                    const uint32_t z = zp ? ((zw_next >> (4 * (g & 7))) & 15u) : 8u;
-                    s2 = sc | (sc << 16);
-                    const uint32_t zm = 0x6400u | z;                        // 1024 + z
-                    zmagic = zm | (zm << 16);
-                    const uint32_t zn = 0xD000u | (z << 4) | 0x0400u;       // -(64 + z)
-                    zneg16 = zn | (zn << 16);
-                    const float qz_max = zp ? fmaxf((float)z, 15.0f - (float)z) : 8.0f;
-                    const float sf = h2f((uint16_t)sc);
-                    if (row_ok && !(sf * qz_max < 65520.0f) && !isnan(sf)) raise_error(kErrRange);
-                    const int gn = g + max(1, step);
-                    if (((long long)gn << lg) < a.K) {
-                        sc_next = __ldg(srow + gn);
-                        if (zp) zw_next = __ldg(zrow + (gn >> 3));
+                for (int i = 0; i < kParts; ++i) {
+                    // (128-byte swizzle: 16-byte unit u of row r sits at u ^ (r % 8))
+                    const uint4 packed =
+                        lds128(wline + ws * C::kWBytes + (uint32_t)(((sb * 2 + part0 + i) ^ (r & 7)) << 4));
+                    const int g = k >> lg;
+                    if (g != g_cur && k < a.K) {       // (codes past K are zeros times X's zeros)
+                        g_cur = g;
+                        const uint32_t sc = sc_next;
+                        const uint32_t z = zp ? ((zw_next >> (4 * (g & 7))) & 15u) : 8u;
+                        s2 = sc | (sc << 16);
+                        const uint32_t zm = 0x6400u | z;                        // 1024 + z
+                        zmagic = zm | (zm << 16);
+                        const uint32_t zn = 0xD000u | (z << 4) | 0x0400u;       // -(64 + z)
+                        zneg16 = zn | (zn << 16);
+                        const float qz_max = zp ? fmaxf((float)z, 15.0f - (float)z) : 8.0f;
+                        const float sf = h2f((uint16_t)sc);
+                        if (row_ok && !(sf * qz_max < 65520.0f) && !isnan(sf)) raise_error(kErrRange);
+                        const int gn = g + gstep;
+                        if (gn < ng) {
+                            sc_next = __ldg(srow + gn);
+                            if (zp) zw_next = __ldg(zrow + (gn >> 3));
+                        }
                     }
-                }
-                uint32_t v[16];
+                    k += kParts == 1 ? kGemmKB : 32;
+                    uint32_t v[16];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t word = w == 0 ? packed[i].x : (w == 1 ? packed[i].y : (w == 2 ? packed[i].z : packed[i].w));
-                    const uint4 d = dequant_word(word, zmagic, zneg16, s2);
-                    v[4 * w] = d.x, v[4 * w + 1] = d.y, v[4 * w + 2] = d.z, v[4 * w + 3] = d.w;
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t word = w == 0 ? packed.x : (w == 1 ? packed.y : (w == 2 ? packed.z : packed.w));
+                        const uint4 d = dequant_word(word, zmagic, zneg16, s2);
+                        v[4 * w] = d.x, v[4 * w + 1] = d.y, v[4 * w + 2] = d.z, v[4 * w + 3] = d.w;
+                    }
+                    // the codes are converted before the wait for the MMAs that read this buffer
+                    if (i == 0) {
+                        ok = ok && __all_sync(0xffffffffu, mbar_wait(&aempty[b], aph ^ 1u));
+                        tc_fence_after();
+                    }
+                    if (ok) tmem_st16(aline + (uint32_t)(b * 64 + i * 16), v);
                 }
-                tmem_st16(abase + ((uint32_t)(q * 32) << 16) + (uint32_t)((b * 2 + h) * 32 + (part0 + i) * 16), v);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&afull[b]);
+                if (++b == C::kABufs) b = 0, aph ^= 1u;
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (sb == kTcWKB - 1 || kb == num_kb - 1) mbar_arrive(&wempty[j % C::kWStages]);
-                mbar_arrive(&afull[b]);
-            }
+            if (lane == 0) mbar_arrive(&wempty[ws]);
+            if (++ws == C::kWStages) ws = 0, wph ^= 1u;
         }
         ok = ok && num_kb > 0 && mbar_wait(tfull, 0);
         ok = __all_sync(0xffffffffu, ok);
@@ -471,7 +484,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         } else {
             float* part = reinterpret_cast<float*>(smem);
             // no k-block of this split (or a time-out, which is flagged): it adds nothing
-            for (int i = threadIdx.x - 96; i < kTcRows * BN; i += 32 * C::kDqWarps) part[i] = 0.0f;
+            for (int i = threadIdx.x - 32 * C::kDqWarp0; i < kTcRows * BN; i += 32 * C::kDqWarps) part[i] = 0.0f;
         }
     }
     if (splits > 1) {
@@ -507,7 +520,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == C::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
