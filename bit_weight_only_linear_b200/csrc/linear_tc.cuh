@@ -11,8 +11,10 @@
 //     shared memory, which at 128 B/cycle otherwise bounds the MMA: per 128 x BN x 16 MMA
 //     (BN / 2 cycles) the shared memory then carries B (BN / 4 cycles), half of the copy of X
 //     (BN / 8) and the packed words (16).
-//   * B = X in the 128-byte-swizzled K-major layout, by tiled TMA (rows in place) or by
-//     tile::gather4 (row numbers from a table: the experts' tokens), into a ring freed by the MMAs.
+//   * B = X in the 128-byte-swizzled K-major layout, in a ring freed by the MMAs: by tiled TMA where
+//     the rows are in place, by 16-byte cp.async where their numbers come from a table (the experts'
+//     tokens; tile::gather4 took 37 cycles per four 128-byte rows whatever the number of issuing
+//     warps, 0.7 of the rate below on a prefill).
 //   * Packed weights: 256-code stages (a whole 128-byte line per row) in a ring of their own,
 //     freed by the dequantisers.
 //   * Few tiles: a cluster of `splits` CTAs shares the K of a tile; the fp32 partial sums meet in
@@ -55,14 +57,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Four rows of a 2-D tensor (box {64, 1}) into four consecutive 128-byte lines.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y0, int y1,
-                                            int y2, int y3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-        "%4, %5, %6, %7}], [%2];" ::"r"(sm100::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(sm100::smem_u32(bar)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
-        : "memory");
+// 16 bytes global -> shared, or zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -92,9 +94,7 @@ struct TcCfg {
     // start and epilogue overlap the other's stream.  Above, one CTA with 16 warps.
     static constexpr int kCtas = BN <= 64 ? 2 : 1;
     static constexpr int kDqWarps = BN <= 64 ? 8 : 16;
-    // Warps that issue the copies of X: a gathered k-block takes BN / 4 copy instructions, a tiled one
-    // takes one.
-    static constexpr int kXWarps = BN >= 64 ? 4 : (BN == 32 ? 2 : 1);
+    static constexpr int kXWarps = BN == 16 ? 1 : 2;      // copy X (a gathered one; a tiled one takes a thread)
     static constexpr int kMmaWarp = kXWarps, kWWarp = kXWarps + 1, kDqWarp0 = kXWarps + 2;
     static constexpr int kThreads = 32 * (kDqWarp0 + kDqWarps);
     static constexpr uint32_t kTmemCols = 512 / kCtas;
@@ -106,10 +106,10 @@ struct TcCfg {
     static constexpr int kWOff = 0;
     static constexpr int kXOff = kWOff + kWStages * kWBytes;
     static constexpr int kRing = kXOff + kXStages * kXBytes;
-    static constexpr int kSrcOff = kRing;                                  // [BN] row numbers of X
+    static constexpr int kSrcOff = kRing;                                  // [BN] row numbers of X (negative: none)
     static constexpr int kBarOff = kSrcOff + BN * 4;
     static constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 2 * kABufs + 1;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8;                // TMEM address, tile
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;                // TMEM address, tile, flags
     static constexpr int kSmemBytes = kMiscOff + 32 + 1024;
     static_assert(kSmemBytes <= (kCtas == 1 ? 232448 : 115712), "shared memory");
     static_assert(2 * BN + kABufs * 64 <= (int)kTmemCols, "tensor memory");
@@ -117,6 +117,8 @@ struct TcCfg {
 };
 
 struct TcArgs {
+    const uint16_t* X;
+    long long ldx;                       // a multiple of 8
     const uint16_t* scales;
     const uint32_t* qzeros;              // NULL: implicit zero 8
     const int32_t* rows;                 // row numbers of X, or NULL
@@ -197,7 +199,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kXStages; ++s) {
-            mbar_init(&xfull[s], 1);
+            mbar_init(&xfull[s], a.rows ? 32 * C::kXWarps : 1);
             mbar_init(&xempty[s], 1);
         }
         for (int s = 0; s < C::kWStages; ++s) {
@@ -232,16 +234,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             misc[3] = (uint32_t)t.z;
             misc[4] = (uint32_t)t.w;
         }
-        if (t.x >= 0)
+        if (t.x >= 0 && a.rows)
             for (int c = lane; c < BN; c += 32) {
-                const int p = t.y + c;
-                int s = -1;
-                if (p < t.z) {
-                    s = a.rows ? __ldg(a.rows + p) : p;
-                    if (s < 0 || s >= a.T) s = -1;
-                }
-                src[c] = s;
+                const int s = t.y + c < t.z ? __ldg(a.rows + t.y + c) : -1;
+                src[c] = s < a.T ? s : -1;
             }
+        if (lane == 0) misc[5] = 0u;
     }
     tc_fence_before();
     __syncthreads();
@@ -259,24 +257,52 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
 
     if (warp < C::kXWarps) {
         // ---------------- X ring ----------------
-        if ((a.rows || warp == 0) && elect_one()) {
+        if (a.rows) {
+            // thread: 16-byte unit u of rows t0, t0 + kXWarps * 4, ..; zeros for rows that do not exist
+            // and past K.  A stage is handed over once the copies of the kAhead stages behind it are
+            // under way: its own have landed then.
+            constexpr int kRowStep = C::kXWarps * 4, kRows = BN / kRowStep, kAhead = C::kXStages - 2;
+            const int u = threadIdx.x & 7, t0 = threadIdx.x >> 3;
+            uint32_t off[kRows];                    // row starts in 16-byte units; all ones: no row
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = num_kb > 0 ? src[t0 + i * kRowStep] : -1;
+                off[i] = r < 0 ? 0xffffffffu : (uint32_t)((unsigned long long)r * (unsigned long long)(a.ldx >> 3));
+            }
+            const uint32_t dst0 = smem_u32(smem + C::kXOff) + (uint32_t)(t0 * 128 + ((u ^ (t0 & 7)) << 4));
+            int s = 0, d = 0;
+            uint32_t ph = 0;
+            for (int j = 0; j < num_kb + kAhead; ++j) {
+                if (j < num_kb) {
+                    mbar_wait_or_abort(&xempty[s], ph ^ 1u, &misc[5]);
+                    const int unit = (kb0 + j) * (kGemmKB / 8) + u;
+                    const bool in_k = unit * 8 < a.K;
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+                        // (rows 4 or 8 apart: the swizzle follows row % 8)
+                        const uint32_t flip = kRowStep % 8 ? (uint32_t)((i & 1) * 64) : 0u;
+                        const bool live = in_k && off[i] != 0xffffffffu;
+                        cp_async16((dst0 ^ flip) + (uint32_t)(s * C::kXBytes + i * kRowStep * 128),
+                                   a.X + (live ? ((size_t)off[i] + unit) * 8 : 0), live);
+                    }
+                    if (++s == C::kXStages) s = 0, ph ^= 1u;
+                }
+                cp_async_commit();
+                if (j >= kAhead) {
+                    cp_async_wait<kAhead>();
+                    fence_proxy_async_smem();       // generic writes -> visible to the MMA
+                    mbar_arrive(&xfull[d]);
+                    if (++d == C::kXStages) d = 0;
+                }
+            }
+            cp_async_wait<0>();
+        } else if (warp == 0 && elect_one()) {
             int issued = 0, s = 0;
             uint32_t ph = 0;
             for (int j = 0; j < num_kb; ++j) {
                 if (!mbar_wait(&xempty[s], ph ^ 1u)) break;
-                uint8_t* dst = smem + C::kXOff + s * C::kXBytes;
-                if (warp == 0) mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
-                if (a.rows) {
-                    // rows that do not exist are read from row 0; their columns are never stored
-                    // (or are stored as those of a row of zeros)
-                    for (int c = warp; c < BN / 4; c += C::kXWarps) {
-                        const int4 r = *reinterpret_cast<const int4*>(src + 4 * c);
-                        tma_gather4(dst + c * 512, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, max(r.x, 0), max(r.y, 0),
-                                    max(r.z, 0), max(r.w, 0));
-                    }
-                } else {
-                    tma_load_2d(dst, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, r0);
-                }
+                mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
+                tma_load_2d(smem + C::kXOff + s * C::kXBytes, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, r0);
                 ++issued;
                 if (++s == C::kXStages) s = 0, ph ^= 1u;
             }
@@ -358,15 +384,14 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         uint32_t s2 = 0, zmagic = 0x64006400u, zneg16 = 0;
         const uint32_t wline = smem_u32(smem + C::kWOff) + (uint32_t)(h * (C::kWBytes / 2) + r * 128);
         const uint32_t aline = abase + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 32 + part0 * 16);
-        bool ok = true;
         int ws = 0, b = 0;
         uint32_t wph = 0, aph = 0;
-        for (int kb = 0; kb < num_kb && ok; kb += kTcWKB) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&wfull[ws], wph));
-            if (!ok) break;
-#pragma unroll
-            for (int sb = 0; sb < kTcWKB; ++sb) {
-                if (kb + sb >= num_kb) break;
+#pragma unroll 1
+        for (int kb = 0; kb < num_kb; kb += kTcWKB) {
+            mbar_wait_or_abort(&wfull[ws], wph, &misc[5]);
+            const int last = min(kTcWKB, num_kb - kb);
+#pragma unroll 1
+            for (int sb = 0; sb < last; ++sb) {
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) {
                     // (128-byte swizzle: 16-byte unit u of row r sits at u ^ (r % 8))
@@ -375,16 +400,16 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                     const int g = k >> lg;
                     if (g != g_cur && k < a.K) {       // (codes past K are zeros times X's zeros)
                         g_cur = g;
-                        const uint32_t sc = sc_next;
-                        const uint32_t z = zp ? ((zw_next >> (4 * (g & 7))) & 15u) : 8u;
-                        s2 = sc | (sc << 16);
-                        const uint32_t zm = 0x6400u | z;                        // 1024 + z
-                        zmagic = zm | (zm << 16);
-                        const uint32_t zn = 0xD000u | (z << 4) | 0x0400u;       // -(64 + z)
-                        zneg16 = zn | (zn << 16);
-                        const float qz_max = zp ? fmaxf((float)z, 15.0f - (float)z) : 8.0f;
-                        const float sf = h2f((uint16_t)sc);
-                        if (row_ok && !(sf * qz_max < 65520.0f) && !isnan(sf)) raise_error(kErrRange);
+                        const uint32_t z = zp ? (zw_next >> (4 * (g & 7))) & 15u : 8u;
+                        s2 = sc_next * 0x00010001u;
+                        zmagic = 0x64006400u + z * 0x00010001u;              // 1024 + z
+                        zneg16 = 0xD400D400u + z * 0x00100010u;              // -(64 + z)
+                        // 15 scale16 may pass fp16 from 0x6C44 (4368) on: look closer there
+                        if (sc_next >= 0x6C44u && row_ok) {
+                            const float qz_max = zp ? fmaxf((float)z, 15.0f - (float)z) : 8.0f;
+                            const float sf = h2f((uint16_t)sc_next);
+                            if (!(fabsf(sf) * qz_max < 65520.0f) && !isnan(sf)) raise_error(kErrRange);
+                        }
                         const int gn = g + gstep;
                         if (gn < ng) {
                             sc_next = __ldg(srow + gn);
@@ -401,22 +426,22 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                     }
                     // the codes are converted before the wait for the MMAs that read this buffer
                     if (i == 0) {
-                        ok = ok && __all_sync(0xffffffffu, mbar_wait(&aempty[b], aph ^ 1u));
+                        mbar_wait_or_abort(&aempty[b], aph ^ 1u, &misc[5]);
+                        __syncwarp();
                         tc_fence_after();
                     }
-                    if (ok) tmem_st16(aline + (uint32_t)(b * 64 + i * 16), v);
+                    tmem_st16(aline + (uint32_t)(b * 64 + i * 16), v);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&afull[b]);
+                if (lane == 0) mbar_arrive(&afull[b]);
                 if (++b == C::kABufs) b = 0, aph ^= 1u;
             }
             if (lane == 0) mbar_arrive(&wempty[ws]);
             if (++ws == C::kWStages) ws = 0, wph ^= 1u;
         }
-        ok = ok && num_kb > 0 && mbar_wait(tfull, 0);
-        ok = __all_sync(0xffffffffu, ok);
+        const bool ok = __all_sync(0xffffffffu, num_kb > 0 && mbar_wait(tfull, 0) && misc[5] == 0);
         tc_fence_after();
 
         // ---------------- epilogue ----------------
@@ -434,35 +459,45 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                 const float b0 = bias && out_ok ? h2f(bias[nn]) : 0.0f;
                 const float b1 = bias && out_ok && ep.gated ? h2f(bias[F + nn]) : 0.0f;
                 constexpr int CH = BN / kSets < 16 ? 8 : 16;          // columns at a time
-                const uint32_t lanes = (uint32_t)(q * 32) << 16;
-                for (int c = c0; c < c0 + cw; c += CH) {
-                    if (r0 + c >= r1) break;
+                const uint32_t at = acc0 + (ep.gated ? 0 : hh * BN) + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+                for (int c = c0; c < c0 + cw && r0 + c < r1; c += CH) {
                     uint32_t u0[CH], u1[CH];
-                    const uint32_t a0 = acc0 + (ep.gated ? 0 : hh * BN) + lanes + (uint32_t)c;
                     if constexpr (CH == 16) {
-                        tmem_ld16(a0, u0);
-                        if (ep.gated) tmem_ld16(a0 + BN, u1);
+                        tmem_ld16(at + c, u0);
+                        if (ep.gated) tmem_ld16(at + BN + c, u1);
                     } else {
-                        tmem_ld8(a0, u0);
-                        if (ep.gated) tmem_ld8(a0 + BN, u1);
+                        tmem_ld8(at + c, u0);
+                        if (ep.gated) tmem_ld8(at + BN + c, u1);
                     }
+                    const int nv = out_ok ? min(CH, r1 - r0 - c) : 0;       // columns to store
                     float res[CH];
-#pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        res[i] = ep.residual && out_ok && r0 + c + i < r1
-                                     ? h2f(ep.residual[(size_t)(r0 + c + i) * ep.ldr + nn])
-                                     : 0.0f;
-                    tmem_ld_wait();
-                    if (out_ok) {
+                    if (ep.residual) {
+                        const uint16_t* rp = ep.residual + (size_t)(r0 + c) * ep.ldr + nn;
 #pragma unroll
                         for (int i = 0; i < CH; ++i) {
-                            const int m = r0 + c + i;
-                            if (m >= r1) break;
-                            const bool live = !a.rows || src[c + i] >= 0;
-                            float y = apply_act((live ? __uint_as_float(u0[i]) : 0.0f) + b0, ep.act);
-                            if (ep.gated) y *= (live ? __uint_as_float(u1[i]) : 0.0f) + b1;
-                            ep.Y[(size_t)m * ep.ldy + nn] = f2h_rn(y + res[i]);
+                            res[i] = i < nv ? h2f(*rp) : 0.0f;
+                            rp += ep.ldr;
                         }
+                    }
+                    tmem_ld_wait();
+                    float y[CH];
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) y[i] = __uint_as_float(u0[i]) + b0;
+                    apply_act(y, ep.act);
+                    if (ep.gated) {
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) y[i] *= __uint_as_float(u1[i]) + b1;
+                    }
+                    if (ep.residual) {
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) y[i] += res[i];
+                    }
+                    uint16_t* yp = ep.Y + (size_t)(r0 + c) * ep.ldy + nn;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        if (i < nv) *yp = f2h_rn(y[i]);
+                        yp += ep.ldy;
                     }
                 }
             }
@@ -509,11 +544,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                 v0 += ld_cluster(at, s);
                 if (ep.gated) v1 += ld_cluster(at + 512, s);
             }
-            if (a.rows && src[c] < 0) v0 = v1 = 0.0f;
-            float y = apply_act(v0 + (bias ? h2f(bias[nn]) : 0.0f), ep.act);
-            if (ep.gated) y *= v1 + (bias ? h2f(bias[F + nn]) : 0.0f);
-            if (ep.residual) y += h2f(ep.residual[(size_t)m * ep.ldr + nn]);
-            ep.Y[(size_t)m * ep.ldy + nn] = f2h_rn(y);
+            float y[1] = {v0 + (bias ? h2f(bias[nn]) : 0.0f)};
+            apply_act(y, ep.act);
+            if (ep.gated) y[0] *= v1 + (bias ? h2f(bias[F + nn]) : 0.0f);
+            if (ep.residual) y[0] += h2f(ep.residual[(size_t)m * ep.ldr + nn]);
+            ep.Y[(size_t)m * ep.ldy + nn] = f2h_rn(y[0]);
         }
         __syncwarp();
         cluster_sync_all();     // no CTA leaves while another reads its shared memory
@@ -563,18 +598,19 @@ awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
     using C = TcCfg<BN>;
     CUtensorMap tx, tq;
     if (!make_tmap_ld(&tx, l.X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)l.T, (uint64_t)l.K, (uint64_t)l.ldx * 2,
-                      l.rows ? 1 : BN, kGemmKB))
+                      BN, kGemmKB))
         return AWQ_ERR_CUDA;
     if (!make_tmap_ld(&tq, l.qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, (uint64_t)l.E * l.N, (uint64_t)(l.K / 8),
                       (uint64_t)l.K / 2, 128, kTcWKB * kGemmKB / 8))
         return AWQ_ERR_CUDA;
     const void* fn = (const void*)linear_tc_kernel<BN>;
     if (!prepare_kernel(fn)) return AWQ_ERR_CUDA;
-    TcArgs a = {l.scales, l.qzeros, l.rows, l.offsets, l.T, l.R, l.E, l.N, l.K, l.G, 0, 0, 0, l.ep};
+    TcArgs a = {l.X, l.ldx, l.scales, l.qzeros, l.rows, l.offsets, l.T, l.R, l.E, l.N, l.K, l.G, 0, 0, 0, l.ep};
     a.n_tiles = l.ep.gated ? ceil_div(l.N / 2, 128) : ceil_div(l.N, kTcRows);
     a.m_tiles = ceil_div(l.R, BN);
     const int num_kb = ceil_div(l.K, kGemmKB);
     a.kb_per = ceil_div(ceil_div(num_kb, splits), kTcWKB) * kTcWKB;
+    if (l.rows && (unsigned long long)l.T * (unsigned long long)(l.ldx >> 3) >= 0xffffffffull) return AWQ_ERR_UNSUPPORTED;
     // grouped: the experts that have rows add at most one partial tile each
     const long long mt = l.offsets ? (long long)l.R / BN + std::min(l.R, l.E) : a.m_tiles;
     const long long ctas = mt * a.n_tiles * splits;

@@ -75,6 +75,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// The same for warps that must stay converged and cannot leave their loop on a time-out: a wait that
+// runs out sets *abort, and every later wait on that flag returns at once, so the loop runs out
+// quickly (on data that the error word declares invalid).
+__device__ __forceinline__ void mbar_wait_or_abort(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+    const uint32_t a = smem_u32(bar);
+    if (mbar_try_wait(a, parity)) return;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(a, parity)) {
+        if (*abort) return;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            raise_error(kErrTimeout);
+            *abort = 1;
+            return;
+        }
+    }
+}
+
 // A wait that cannot complete: one thread waits on a fresh mbarrier that nothing
 // arrives on, so the bounded wait gives up after kWaitLimitNs and raises the timeout
 // flag (awq_check_bounded_wait).
