@@ -336,42 +336,44 @@ def _config(group_size: int, zero_point: bool) -> QuantConfig:
     return c
 
 
-def _rows(t: Optional[torch.Tensor], name: str, device, shape, dtype=torch.float16):
+def _refuse(t, name, index, shape, dtypes, what):
+    """Raise the ValueError that says which of a tensor's properties is wrong."""
+    if t.get_device() != index or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be on cuda:{index} with dtype one of {dtypes}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must {what}")
+
+
+def _rows(t: Optional[torch.Tensor], name: str, index: int, shape, dtypes=_F16):
     """(data pointer, distance of rows in elements) of a 2-D tensor with contiguous rows."""
     if t is None:
         return 0, 0
-    if t.device != device or t.dtype is not dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    rows, cols = shape
+    if t.get_device() != index or t.dtype not in dtypes or t.shape != shape:
+        _refuse(t, name, index, shape, dtypes, "")
     ld, inner = t.stride()
-    if rows <= 1:
-        ld = max(cols, 8 * ((cols + 7) // 8))
-    if (inner != 1 and cols > 1) or ld < cols:
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    cols = shape[1]
+    if shape[0] <= 1:
+        ld = (cols + 7) // 8 * 8       # one row or none: any distance does
+    if ld < cols or (inner != 1 and cols > 1):
+        _refuse(t, name, index, shape, dtypes, "have contiguous rows that do not overlap")
     return t.data_ptr(), ld
 
 
-def _flat(t: Optional[torch.Tensor], name: str, device, shape, dtypes) -> int:
+def _flat(t: Optional[torch.Tensor], name: str, index: int, shape, dtypes) -> int:
     """Data pointer of a contiguous tensor of the given shape."""
     if t is None:
         return 0
-    if t.device != device or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be on {device} with dtype one of {dtypes}, got {t.dtype} on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, index, shape, dtypes, "be contiguous")
     return t.data_ptr()
 
 
-def _on(device, fn_name: str, stream, *args) -> None:
-    """Call the entry point with `device` current, on `stream` or the device's current stream."""
+def _on(index: int, fn_name: str, stream, *args) -> None:
+    """Call the entry point with device `index` current, on `stream` or the device's current stream."""
     fn = getattr(_lib or load_library(), fn_name)
-    index = device.index
     st = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, st)
     else:
         with torch.cuda.device(index):
@@ -385,7 +387,7 @@ def _cuda(t: torch.Tensor, name: str, dims: int = 2):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    return t.device
+    return t.get_device()
 
 
 def _activation(activation) -> int:
@@ -395,18 +397,18 @@ def _activation(activation) -> int:
     return code
 
 
-def _weights(lead, qweight, scales, qzeros, K, group_size, zero_point, device):
-    """(N, pointers) of packed weights with the leading axes `lead` (() or (E,))."""
-    if qweight.dim() != len(lead) + 2 or qweight.shape[-1] * 8 != K or qweight.shape[:-2] != lead:
-        raise ValueError(f"qweight has shape {tuple(qweight.shape)}, expected {[*lead, 'N', K // 8]}")
-    if zero_point != (qzeros is not None):
+def _weights(lead, qweight, scales, qzeros, K, group_size, zero_point, index):
+    """(N, data pointers) of packed weights with the leading axes `lead` (() or (E,))."""
+    shape = qweight.shape
+    if len(shape) != len(lead) + 2 or shape[-1] * 8 != K or shape[:-2] != lead:
+        raise ValueError(f"qweight has shape {tuple(shape)}, expected {[*lead, 'N', K // 8]}")
+    if zero_point == (qzeros is None):
         raise ValueError("qzeros must be given with zero_point and left out without")
     if group_size not in (32, 64, 128, 256) or K % group_size:
         raise ValueError(f"group_size {group_size} is not 32, 64, 128 or 256, or does not divide K = {K}")
-    N, ng = qweight.shape[-2], K // group_size
-    return N, (_flat(qweight, "qweight", device, (*lead, N, K // 8), _W32),
-               _flat(scales, "scales", device, (*lead, N, ng), _F16),
-               _flat(qzeros, "qzeros", device, (*lead, N, (ng + 7) // 8), _W32))
+    N, ng = shape[-2], K // group_size
+    return (N, _flat(qweight, "qweight", index, shape, _W32), _flat(scales, "scales", index, (*lead, N, ng), _F16),
+            _flat(qzeros, "qzeros", index, (*lead, N, (ng + 7) // 8), _W32))
 
 
 def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bias=None, activation=None,
@@ -416,20 +418,20 @@ def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bi
     gated: W holds the gate's N/2 rows, then the other half's; Y [M][N/2] = act(gate) * other
     (+ residual).  activation: None/"none", "relu", "silu", "gelu" (erf) or "gelu_tanh".
     X, residual and out may have strided rows (X: 16-byte aligned rows); residual may be out."""
-    device = _cuda(X, "X")
+    dev = _cuda(X, "X")
     M, K = X.shape
-    N, (pq, ps, pz) = _weights((), qweight, scales, qzeros, K, group_size, zero_point, device)
+    N, pq, ps, pz = _weights((), qweight, scales, qzeros, K, group_size, zero_point, dev)
     act = _activation(activation)
     if gated and N & 1:
         raise ValueError("a gated linear needs an even number of weight rows")
     n_out = N // 2 if gated else N
     if out is None:
-        out = torch.empty((M, n_out), dtype=torch.float16, device=device)
-    px, ldx = _rows(X, "X", device, (M, K))
-    pr, ldr = _rows(residual, "residual", device, (M, n_out))
-    py, ldy = _rows(out, "out", device, (M, n_out))
-    _on(device, "awq_linear_fused", stream, px, M, ldx, pq, ps, pz, N, K, _config(group_size, zero_point),
-        _flat(bias, "bias", device, (N,), _F16), act, 1 if gated else 0, pr, ldr, py, ldy)
+        out = X.new_empty((M, n_out))
+    px, ldx = _rows(X, "X", dev, (M, K))
+    pr, ldr = _rows(residual, "residual", dev, (M, n_out))
+    py, ldy = _rows(out, "out", dev, (M, n_out))
+    _on(dev, "awq_linear_fused", stream, px, M, ldx, pq, ps, pz, N, K, _config(group_size, zero_point),
+        _flat(bias, "bias", dev, (N,), _F16), act, 1 if gated else 0, pr, ldr, py, ldy)
     return out
 
 
@@ -444,22 +446,22 @@ def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=12
 
     Row p reads row rows[p] of X (int32 [R]; R = len(rows)), or row p where rows is None (R = len(X)).
     Rows that no expert owns are left as they are in `out` (uninitialised without one)."""
-    device = _cuda(X, "X")
+    dev = _cuda(X, "X")
     T, K = X.shape
     E = qweight.shape[0]
-    N, (pq, ps, pz) = _weights((E,), qweight, scales, qzeros, K, group_size, zero_point, device)
+    N, pq, ps, pz = _weights((E,), qweight, scales, qzeros, K, group_size, zero_point, dev)
     act = _activation(activation)
     if gated and N & 1:
         raise ValueError("a gated linear needs an even number of weight rows")
     n_out = N // 2 if gated else N
     R = T if rows is None else rows.shape[0]
     if out is None:
-        out = torch.empty((R, n_out), dtype=torch.float16, device=device)
-    px, ldx = _rows(X, "X", device, (T, K))
-    py, ldy = _rows(out, "out", device, (R, n_out))
-    _on(device, "awq_linear_grouped", stream, px, T, ldx, _flat(rows, "rows", device, (R,), _I32), R,
-        _flat(offsets, "offsets", device, (E + 1,), _I32), E, pq, ps, pz, N, K, _config(group_size, zero_point),
-        _flat(bias, "bias", device, (E, N), _F16), act, 1 if gated else 0, py, ldy)
+        out = X.new_empty((R, n_out))
+    px, ldx = _rows(X, "X", dev, (T, K))
+    py, ldy = _rows(out, "out", dev, (R, n_out))
+    _on(dev, "awq_linear_grouped", stream, px, T, ldx, _flat(rows, "rows", dev, (R,), _I32), R,
+        _flat(offsets, "offsets", dev, (E + 1,), _I32), E, pq, ps, pz, N, K, _config(group_size, zero_point),
+        _flat(bias, "bias", dev, (E, N), _F16), act, 1 if gated else 0, py, ldy)
     return out
 
 
@@ -478,41 +480,45 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
               workspace: Optional[torch.Tensor] = None, stream=None) -> MoeRoute:
     """awq_moe_route: each token's top_k experts by logits [T][E] (fp32 or fp16; -inf masks an
     expert), their weights, and the order of the rows by expert for linear_grouped / moe_combine."""
-    device = _cuda(logits, "logits")
+    dev = _cuda(logits, "logits")
     T, E = logits.shape
-    if logits.dtype not in (torch.float32, torch.float16):
-        raise ValueError(f"logits has dtype {logits.dtype}, expected float32 or float16")
+    half = logits.dtype is torch.float16
     score = SCORINGS.get(scoring)
     if score is None:
         raise ValueError(f"scoring {scoring!r} is not one of {sorted(SCORINGS)}")
-    pl, ld = _rows(logits, "logits", device, (T, E), logits.dtype)
+    pl, ld = _rows(logits, "logits", dev, (T, E), _LOGITS)
     if out is None:
-        # one allocation for the five outputs: 16-byte aligned parts of an int32 buffer
-        n, k = T * top_k, top_k
-        a = (n + 3) // 4 * 4
-        buf = torch.empty(4 * a + E + 1, dtype=torch.int32, device=device)
-        out = MoeRoute(buf[:n].view(torch.float32).view(T, k), buf[a:a + n].view(T, k), buf[4 * a:],
-                       buf[2 * a:2 * a + n], buf[3 * a:3 * a + n].view(T, k))
-    need = _route_need(T, E, device) if workspace is None else 0
-    if need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:   # freed on return: not to be reused before `stream` has passed the kernels
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(_stream(stream), device=device))
+        experts, positions, rows = logits.new_empty((3, T, top_k), dtype=torch.int32).unbind()
+        out = MoeRoute(logits.new_empty((T, top_k), dtype=torch.float32), experts,
+                       logits.new_empty(E + 1, dtype=torch.int32), rows.view(-1), positions)
+    weights, experts, offsets, rows, positions = out
+    slots = (T, top_k)
+    if workspace is None:
+        need = _route_need(T, E, dev)
+        if need:
+            workspace = logits.new_empty(need, dtype=torch.uint8)
+            if stream is not None:   # freed on return: not to be reused before `stream` has passed the kernels
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                        else torch.cuda.ExternalStream(_stream(stream), device=logits.device))
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _on(device, "awq_moe_route", stream, pl, 1 if logits.dtype is torch.float16 else 0, T, ld, E, top_k, score,
-        1 if renormalize else 0, _flat(out.weights, "weights", device, (T, top_k), (torch.float32,)),
-        _flat(out.experts, "experts", device, (T, top_k), _I32), _flat(out.offsets, "offsets", device, (E + 1,), _I32),
-        _flat(out.rows, "rows", device, (T * top_k,), _I32),
-        _flat(out.positions, "positions", device, (T, top_k), _I32), ws, ws_bytes)
+    _on(dev, "awq_moe_route", stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0,
+        _flat(weights, "weights", dev, slots, _F32), _flat(experts, "experts", dev, slots, _I32),
+        _flat(offsets, "offsets", dev, (E + 1,), _I32), _flat(rows, "rows", dev, (T * top_k,), _I32),
+        _flat(positions, "positions", dev, slots, _I32), ws, ws_bytes)
     return out
 
 
-def _route_need(T: int, E: int, device) -> int:
+_F32, _LOGITS = (torch.float32,), (torch.float32, torch.float16)
+_ROUTE_SINGLE = 256      # tokens up to which routing is one block and needs no workspace
+
+
+def _route_need(T: int, E: int, index: int) -> int:
+    if T <= _ROUTE_SINGLE:
+        return 0
     lib = _lib or load_library()
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == index:
         return lib.awq_moe_route_workspace_bytes(T, E)
-    with torch.cuda.device(device.index):
+    with torch.cuda.device(index):
         return lib.awq_moe_route_workspace_bytes(T, E)
 
 
@@ -520,16 +526,16 @@ def moe_combine(Y, weights, positions, residual=None, out=None, stream=None) -> 
     """awq_moe_combine: out[t] = residual[t] + sum_j weights[t][j] Y[positions[t][j]] (positions
     outside Y contribute nothing).  Y [R][N], weights fp32 / positions int32 [T][k]; Y, residual and
     out may have strided rows; residual may be out."""
-    device = _cuda(Y, "Y")
+    dev = _cuda(Y, "Y")
     R, N = Y.shape
     if positions.dim() != 2:
         raise ValueError("positions must have 2 dimensions")
-    T, k = positions.shape
+    T, k = slots = positions.shape
     if out is None:
-        out = torch.empty((T, N), dtype=torch.float16, device=device)
-    py, ldy = _rows(Y, "Y", device, (R, N))
-    pr, ldr = _rows(residual, "residual", device, (T, N))
-    po, ldo = _rows(out, "out", device, (T, N))
-    _on(device, "awq_moe_combine", stream, py, R, ldy, _flat(weights, "weights", device, (T, k), (torch.float32,)),
-        _flat(positions, "positions", device, (T, k), _I32), T, k, N, pr, ldr, po, ldo)
+        out = Y.new_empty((T, N))
+    py, ldy = _rows(Y, "Y", dev, (R, N))
+    pr, ldr = _rows(residual, "residual", dev, (T, N))
+    po, ldo = _rows(out, "out", dev, (T, N))
+    _on(dev, "awq_moe_combine", stream, py, R, ldy, _flat(weights, "weights", dev, slots, _F32),
+        _flat(positions, "positions", dev, slots, _I32), T, k, N, pr, ldr, po, ldo)
     return out

@@ -16,6 +16,7 @@
 #include "gemm_sm100.cuh"
 #include "search.cuh"
 #include "clip.cuh"
+#include "linear_decode.cuh"
 #include "linear_tc.cuh"
 #include "moe.cuh"
 
@@ -298,10 +299,10 @@ awq_status check_fused(const uint16_t* X, int M, int64_t ldx, const uint32_t* qw
     return (two & 1) ? AWQ_ERR_INVALID_ARG : AWQ_OK;
 }
 
-awq_status launch_linear(const LinearArgs& l, cudaStream_t st) {
+awq_status run_linear(const LinearArgs& l, cudaStream_t st) {
     DeviceInfo d;
     if (!device_info(d)) return AWQ_ERR_CUDA;
-    return launch_linear_tc(l, d.sms, st);
+    return launch_linear(l, d, st);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -321,7 +322,7 @@ awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uin
     const Epilogue ep = {bias, residual, (long long)ldr, Y, (long long)ldy, activation, gated};
     const LinearArgs l = {X, M, (long long)ldx, nullptr, M, nullptr, 1, qweight, scales,
                           cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep};
-    return launch_linear(l, (cudaStream_t)stream);
+    return run_linear(l, (cudaStream_t)stream);
 }
 
 awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const int32_t* rows, int32_t R,
@@ -340,7 +341,7 @@ awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const i
     const Epilogue ep = {bias, nullptr, 0, Y, (long long)ldy, activation, gated};
     const LinearArgs l = {X, T, (long long)ldx, rows, R, offsets, E, qweight, scales,
                           cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep};
-    return launch_linear(l, (cudaStream_t)stream);
+    return run_linear(l, (cudaStream_t)stream);
 }
 
 size_t awq_moe_route_workspace_bytes(int32_t T, int32_t E) {

@@ -1,0 +1,464 @@
+// Fused linear and expert-grouped linear for few rows (decode): HBM-bound streaming of the packed
+// weights past the rows of X, multiplied with mma.sync straight from registers.
+//
+// The arithmetic is the GEMV's (gemv.cuh): a mask turns two adjacent codes into fp16 subnormals
+// q 2^-24 (or 16 q 2^-24), m16n8k16 multiplies them exactly with up to 8 rows of X, and the group's
+// scale and zero point are applied once per k-step in fp32, so no weight is rounded:
+//     y += (scale16 2^24) (D1 + D16 / 16) - (scale16 z) sum_k x.
+// What differs is the shape of the work:
+//   * A unit is 32 weight rows (two MMA row tiles) by the whole K.  The two tiles share every X
+//     fragment, which halves the shared-memory reads of X per weight (they, not the weights, bound
+//     the 16-row form at 8 rows).  Gated, the tiles are 16 gate rows and the 16 rows F behind them,
+//     so both halves of an output meet in one unit's partial sums.
+//   * A persistent CTA per SM takes a contiguous range of units: all of one dense matrix, or the
+//     units of the experts that have rows (8 rows of an expert at a time), so that X is staged once
+//     per expert and CTA.
+//   * Warps: a producer (3-D TMA, 32 KB stages of 32 rows x 2048 codes), a converter (scales and
+//     zeros -> fp32 pairs per stage), 16 consumers (128 codes of a stage each), a reducer (the
+//     consumers' partial sums in a fixed order, then the epilogue).
+// K must be a multiple of 128.  Every wait is bounded.
+#pragma once
+
+#include "common.cuh"
+#include "epilogue.cuh"
+#include "gemv.cuh"
+#include "gemv_launch.cuh"
+#include "linear_tc.cuh"
+#include "sm100.cuh"
+
+namespace awq {
+
+constexpr int kDecConsumers = 16;
+constexpr int kDecThreads = (3 + kDecConsumers) * 32;
+constexpr int kDecRows = 32;                     // weight rows per unit
+constexpr int kDecKC = 2048;                     // codes per row and stage
+constexpr int kDecStageBytes = kDecRows * kDecKC / 2;
+constexpr int kDecMaxRows = 8;                   // rows of X at a time (MMA N)
+constexpr int kDecPartPitch = 36;                // words per row of X in a partial sum (bank spread)
+
+struct DecSmem {
+    int K, M, S, Kp, nsteps, gpc;
+    __host__ __device__ DecSmem(int M_, int K_, int G, int S_) : K(K_), M(M_), S(S_) {
+        Kp = (K + kDecKC - 1) / kDecKC * kDecKC;
+        nsteps = Kp / (32 * gemv_words_per_thread(G));
+        gpc = kDecKC / G;
+    }
+    // converted (scale, scale * zero) pairs of a stage: [32 rows][gpc], rows padded by 16 bytes
+    __host__ __device__ int cvt_pitch() const { return gpc * 8 + 16; }
+    __host__ __device__ int cvt() const { return S * kDecStageBytes; }
+    __host__ __device__ int x() const { return cvt() + S * kDecRows * cvt_pitch(); }
+    __host__ __device__ int x_pitch() const { return Kp * 2 + 64; }
+    __host__ __device__ int xsum() const { return x() + M * x_pitch(); }
+    __host__ __device__ int part() const { return (xsum() + M * nsteps * 4 + 15) & ~15; }
+    __host__ __device__ int part_stride() const { return kDecConsumers * M * kDecPartPitch * 4; }
+    __host__ __device__ int bars() const { return part() + 2 * part_stride(); }
+    // full[S], empty[S], rfull[2], rempty[2]
+    __host__ __device__ int bytes() const { return bars() + (2 * S + 4) * 8 + 128; }
+};
+
+struct DecArgs {
+    const uint16_t* X;
+    long long ldx;
+    const uint16_t* scales;
+    const uint32_t* qzeros;              // NULL: implicit zero 8
+    const int32_t* rows;                 // row numbers of X, or NULL
+    const int32_t* offsets;              // [E+1], or NULL: one range of R rows
+    int T, R, E, N, K;
+    int units;                           // units of one matrix
+    int mc;                              // rows of X at a time
+    int S;                               // stages
+    Epilogue ep;
+};
+
+// A run of units of one matrix with one set of rows.
+struct DecSeg {
+    int expert, r0, nr, n, count;        // rows r0 .. r0+nr-1; units n .. n+count-1
+};
+
+// Row sets (of up to mc rows) of all experts, by a whole warp.
+__device__ __forceinline__ int dec_sets(const DecArgs& a) {
+    if (!a.offsets) return ceil_div(a.R, a.mc);
+    int t = 0;
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+        const int2 g = expert_range(a.offsets, e, a.R);
+        t += (g.y - g.x + a.mc - 1) / a.mc;
+    }
+    return __reduce_add_sync(0xffffffffu, t);
+}
+
+// The segment that starts at unit u (of all sets' units, set by set), at most up to unit `end`.
+__device__ __forceinline__ DecSeg dec_segment(const DecArgs& a, int u, int end) {
+    const int set = u / a.units;
+    DecSeg s;
+    s.n = u - set * a.units;
+    s.count = min(a.units - s.n, end - u);
+    if (a.offsets) {
+        const int4 t = find_tile(a.offsets, a.E, a.R, a.mc, 1, set);
+        s.expert = t.x;
+        s.r0 = t.y;
+        s.nr = min(a.mc, t.z - t.y);
+    } else {
+        s.expert = 0;
+        s.r0 = set * a.mc;
+        s.nr = min(a.mc, a.R - s.r0);
+    }
+    return s;
+}
+
+template <int G>
+__global__ void __launch_bounds__(kDecThreads, 1)
+linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a) {
+    using namespace sm100;
+    constexpr int WT = gemv_words_per_thread(G);
+    constexpr int kStepCodes = 32 * WT;
+    constexpr int Q = 128 / kStepCodes;                    // k-steps of a consumer per stage
+    constexpr int GPC = kDecKC / G;                        // groups per stage
+    extern __shared__ __align__(128) uint8_t smem[];
+    const DecSmem L(a.mc, a.K, G, a.S);
+    const int S = a.S;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars());   // weights and converted pairs in
+    uint64_t* empty = full + S;                    // consumers done with a stage
+    uint64_t* rfull = empty + S;                   // partial sums of a unit written
+    uint64_t* rempty = rfull + 2;                  // reducer done with the slot
+    volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(rempty + 2);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 2);                // producer (with its bytes) + converter
+            mbar_init(&empty[i], kDecConsumers);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&rfull[i], kDecConsumers);
+            mbar_init(&rempty[i], 1);
+        }
+        *abort = 0;
+        mbar_fence_init();
+        prefetch_tensormap(&tmap_q);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+
+    // this CTA's units, of all row sets' units
+    const long long total = (long long)dec_sets(a) * a.units;
+    const int u_begin = (int)(total * blockIdx.x / gridDim.x), u_end = (int)(total * (blockIdx.x + 1) / gridDim.x);
+    const int nchunks = L.Kp / kDecKC;
+    const int F = a.ep.gated ? a.N / 2 : a.N;
+    // first rows of the two row tiles of unit n
+    auto tile0 = [&](int n) { return a.ep.gated ? n * 16 : n * kDecRows; };
+    auto tile1 = [&](int n) { return a.ep.gated ? F + n * 16 : n * kDecRows + 16; };
+
+    if (warp == 0) {
+        // ---------------- producer ----------------
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = u_begin; u < u_end && ok;) {
+            const DecSeg sg = dec_segment(a, u, u_end);
+            u += sg.count;
+            for (int n = sg.n; n < sg.n + sg.count && ok; ++n) {
+                const int ra = sg.expert * a.N + tile0(n), rb = sg.expert * a.N + tile1(n);
+                for (int c = 0; c < nchunks; ++c) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        uint8_t* dst = smem + (size_t)st * kDecStageBytes;
+                        // boxes {16 words, 16 rows, 16 blocks of 128 codes}; blocks past K are zeros
+                        mbar_arrive_expect_tx(&full[st], kDecStageBytes);
+                        tma_load_3d(dst, &tmap_q, &full[st], 0, ra, c * (kDecKC / 128));
+                        tma_load_3d(dst + kDecStageBytes / 2, &tmap_q, &full[st], 0, rb, c * (kDecKC / 128));
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++st == S) st = 0, ph ^= 1u;
+                }
+            }
+        }
+        // copies in flight must land before the CTA exits
+        for (int j = issued - 1; j >= 0 && j >= issued - S; --j) mbar_wait(&full[j % S], (j / S) & 1);
+        return;
+    }
+    if (warp == 1) {
+        // ---------------- converter: lane = row of the unit; scales and zero words of the next stage
+        // are fetched while the current one waits ----------------
+        constexpr int OCT = GPC / 8;                           // octets of groups per row and stage
+        const int ng = a.K / G, nzw = ceil_div(ng, 8);
+        const bool zp = a.qzeros != nullptr;
+        const bool vec = (ng & 7) == 0;                        // 16-byte aligned scale rows
+        uint4 sc[OCT];
+        uint32_t zw[OCT];
+        auto fetch = [&](int expert, int n, int c) {
+            const int row = lane < 16 ? tile0(n) + lane : tile1(n) + lane - 16;
+            const int lim = a.ep.gated && lane < 16 ? F : a.N;
+            const size_t wr = (size_t)expert * a.N + min(row, lim - 1);   // rows past the end: dropped later
+            const uint16_t* sp = a.scales + wr * ng;
+#pragma unroll
+            for (int o = 0; o < OCT; ++o) {
+                const int g0 = c * GPC + 8 * o;
+                sc[o] = make_uint4(0u, 0u, 0u, 0u);                       // groups past K: scale 0
+                zw[o] = 0x88888888u;
+                if (g0 < ng) {
+                    if (vec) {
+                        sc[o] = __ldg(reinterpret_cast<const uint4*>(sp + g0));
+                    } else {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[i] = g0 + i < ng ? __ldg(sp + g0 + i) : 0u;
+                        sc[o] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                    }
+                    if (zp) zw[o] = __ldg(a.qzeros + wr * nzw + (g0 >> 3));
+                }
+            }
+        };
+        int st = 0;
+        uint32_t ph = 0;
+        for (int u = u_begin; u < u_end;) {
+            const DecSeg sg = dec_segment(a, u, u_end);
+            u += sg.count;
+            fetch(sg.expert, sg.n, 0);
+            for (int n = sg.n; n < sg.n + sg.count; ++n) {
+                for (int c = 0; c < nchunks; ++c) {
+                    mbar_wait_or_abort(&empty[st], ph ^ 1u, abort);
+                    float4* dst = reinterpret_cast<float4*>(smem + L.cvt() + (st * kDecRows + lane) * L.cvt_pitch());
+#pragma unroll
+                    for (int o = 0; o < OCT; ++o) {
+                        const uint32_t hw[4] = {sc[o].x, sc[o].y, sc[o].z, sc[o].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float s0 = h2f((uint16_t)(hw[k] & 0xFFFFu)), s1 = h2f((uint16_t)(hw[k] >> 16));
+                            const float z0 = (float)((zw[o] >> (8 * k)) & 15u), z1 = (float)((zw[o] >> (8 * k + 4)) & 15u);
+                            dst[o * 4 + k] = make_float4(s0 * 16777216.0f, s0 * z0, s1 * 16777216.0f, s1 * z1);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[st]);
+                    if (++st == S) st = 0, ph ^= 1u;
+                    if (c + 1 < nchunks) fetch(sg.expert, n, c + 1);
+                    else if (n + 1 < sg.n + sg.count) fetch(sg.expert, n + 1, 0);
+                }
+            }
+        }
+        return;
+    }
+    if (warp == 2) {
+        // ---------------- reducer: lane = row of the unit; the consumers' sums in order, the epilogue ----------------
+        const Epilogue& ep = a.ep;
+        int b = 0;
+        uint32_t ph = 0;
+        for (int u = u_begin; u < u_end;) {
+            const DecSeg sg = dec_segment(a, u, u_end);
+            u += sg.count;
+            const uint16_t* bias = ep.bias ? ep.bias + (size_t)sg.expert * a.N : nullptr;
+            for (int n = sg.n; n < sg.n + sg.count; ++n) {
+                const int row = lane < 16 ? tile0(n) + lane : tile1(n) + lane - 16;
+                const int lim = ep.gated && lane < 16 ? F : a.N;
+                const float bv = bias && row < lim ? h2f(__ldg(bias + row)) : 0.0f;
+                const bool store = row < lim && (!ep.gated || lane < 16);
+                mbar_wait_or_abort(&rfull[b], ph, abort);
+                __syncwarp();
+                const float* slot = reinterpret_cast<const float*>(smem + L.part() + b * L.part_stride()) + lane;
+                for (int m = 0; m < sg.nr; ++m) {
+                    float res = 0.0f;
+                    if (ep.residual && store) res = h2f(ep.residual[(size_t)(sg.r0 + m) * ep.ldr + row]);
+                    float acc = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kDecConsumers; ++w) acc += slot[(w * a.mc + m) * kDecPartPitch];
+                    acc += bv;
+                    const float other = __shfl_down_sync(0xffffffffu, acc, 16);
+                    float y[1] = {acc};
+                    apply_act(y, ep.act);
+                    if (ep.gated) y[0] *= other;
+                    if (store) ep.Y[(size_t)(sg.r0 + m) * ep.ldy + row] = f2h_rn(y[0] + res);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rempty[b]);
+                if (++b == 2) b = 0, ph ^= 1u;
+            }
+        }
+        return;
+    }
+
+    // ---------------- consumers ----------------
+    constexpr int kCons = kDecConsumers * 32;
+    constexpr int R = G >= kStepCodes ? G / kStepCodes : 1;     // k-steps per group
+    constexpr int TPS = 4 * WT;                                  // 16-byte chunks per k-step
+    const int cw = warp - 3, ct = threadIdx.x - 96;
+    const int g = lane >> 2, t = lane & 3;
+    const int pitch = L.x_pitch();
+    uint8_t* xs = smem + L.x();
+    float* xsum = reinterpret_cast<float*>(smem + L.xsum());
+    const uint32_t sbase = smem_u32(smem);
+    // weights: row r of a tile, block b of 128 codes: [b][r][64 bytes]; this warp's block is cw
+    const uint32_t wofs = (uint32_t)(cw * 1024 + g * 64 + t * WT * 4);
+    const uint32_t cofs = smem_u32(smem + L.cvt()) + (uint32_t)(g * L.cvt_pitch() + (cw * 128 / G) * 8);
+    const uint32_t crow8 = 8u * L.cvt_pitch(), cstage = (uint32_t)(kDecRows * L.cvt_pitch());
+    const int m0 = 2 * t, m1 = 2 * t + 1;
+    int st = 0, b = 0;
+    uint32_t ph = 0, rph = 0;
+    for (int u = u_begin; u < u_end;) {
+        const DecSeg sg = dec_segment(a, u, u_end);
+        u += sg.count;
+        // X of the segment: 16-byte chunks reordered within each k-step to [j][t] with the middle words
+        // swapped (so that a fragment is a register pair of one 16-byte read), zeros past K and for rows
+        // that do not exist; per-k-step sums of x
+        asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory");       // the previous segment's X is done with
+        {
+            const int kwp = L.Kp >> 3, kwv = a.K >> 3;                 // kwp is a multiple of 256
+            for (int m = 0; m < sg.nr; ++m) {
+                int src = sg.r0 + m;
+                if (a.rows) src = __ldg(a.rows + src);
+                const bool live = src >= 0 && src < a.T;
+                const uint4* row = reinterpret_cast<const uint4*>(a.X + (live ? src : 0) * a.ldx);
+                uint4* dst = reinterpret_cast<uint4*>(xs + m * pitch);
+                for (int word = ct; word < kwp; word += kCons) {
+                    const uint4 v = live && word < kwv ? __ldg(row + word) : make_uint4(0u, 0u, 0u, 0u);
+                    const int s = word / TPS, r = word % TPS;
+                    const int tt = r / WT, j = r % WT;
+                    dst[(s * WT + j) * 4 + tt] = make_uint4(v.x, v.z, v.y, v.w);
+                    const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+                    float acc = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc += h2f(h[e]);
+#pragma unroll
+                    for (int o = TPS / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                    if (r == 0) xsum[m * L.nsteps + s] = acc;
+                }
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory");
+        // lanes whose column is no row of X read row 0; their sums are not stored
+        const uint32_t xrow = smem_u32(xs + (g < sg.nr ? g : 0) * pitch) + (uint32_t)(t * 16 + cw * Q * WT * 64);
+        const uint32_t xs0 = smem_u32(xsum + (m0 < sg.nr ? m0 : 0) * L.nsteps + cw * Q);
+        const uint32_t xs1 = smem_u32(xsum + (m1 < sg.nr ? m1 : 0) * L.nsteps + cw * Q);
+        for (int n = 0; n < sg.count; ++n) {
+            float y[2][4] = {};
+            for (int c = 0; c < nchunks; ++c) {
+                mbar_wait_or_abort(&full[st], ph, abort);
+                __syncwarp();
+                const uint32_t wb = sbase + (uint32_t)(st * kDecStageBytes) + wofs;
+                const uint32_t cv = cofs + (uint32_t)st * cstage;
+                const uint32_t xb = xrow + (uint32_t)(c * (kDecKC / kStepCodes) * WT * 64);
+                const uint32_t x0b = xs0 + (uint32_t)(c * (kDecKC / kStepCodes) * 4);
+                const uint32_t x1b = xs1 + (uint32_t)(c * (kDecKC / kStepCodes) * 4);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    uint32_t wa[2][WT], wc[2][WT];
+                    float d1[2][4], d16[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        lds_words<WT>(wb + h * (kDecStageBytes / 2) + q * WT * 16, wa[h]);
+                        lds_words<WT>(wb + h * (kDecStageBytes / 2) + 512 + q * WT * 16, wc[h]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < WT; ++j) {
+                        const uint4 x = lds128(xb + (uint32_t)((q * WT + j) * 64));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t p = wa[h][j], r = wc[h][j], p8 = p >> 8, r8 = r >> 8;
+                            if (j == 0) {
+                                mma_16816_first(d1[h], p & 0x000F000Fu, r & 0x000F000Fu, p8 & 0x000F000Fu,
+                                                r8 & 0x000F000Fu, x.x, x.y);
+                                mma_16816_first(d16[h], p & 0x00F000F0u, r & 0x00F000F0u, p8 & 0x00F000F0u,
+                                                r8 & 0x00F000F0u, x.z, x.w);
+                            } else {
+                                mma_16816(d1[h], p & 0x000F000Fu, r & 0x000F000Fu, p8 & 0x000F000Fu,
+                                          r8 & 0x000F000Fu, x.x, x.y);
+                                mma_16816(d16[h], p & 0x00F000F0u, r & 0x00F000F0u, p8 & 0x00F000F0u,
+                                          r8 & 0x00F000F0u, x.z, x.w);
+                            }
+                        }
+                    }
+                    const float x0 = ldsf(x0b + (uint32_t)(q * 4)), x1 = ldsf(x1b + (uint32_t)(q * 4));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        // y += (scale 2^24)(D1 + D16 / 16) - (scale z) sum x
+                        const uint32_t at = cv + (uint32_t)((q / R) * 8) + 2u * h * crow8;
+                        const uint2 pa = lds64(at), pb = lds64(at + crow8);
+                        const float sa = __uint_as_float(pa.x), za = __uint_as_float(pa.y);
+                        const float sb = __uint_as_float(pb.x), zb = __uint_as_float(pb.y);
+                        y[h][0] = fmaf(sa, fmaf(d16[h][0], 0.0625f, d1[h][0]), fmaf(-za, x0, y[h][0]));
+                        y[h][1] = fmaf(sa, fmaf(d16[h][1], 0.0625f, d1[h][1]), fmaf(-za, x1, y[h][1]));
+                        y[h][2] = fmaf(sb, fmaf(d16[h][2], 0.0625f, d1[h][2]), fmaf(-zb, x0, y[h][2]));
+                        y[h][3] = fmaf(sb, fmaf(d16[h][3], 0.0625f, d1[h][3]), fmaf(-zb, x1, y[h][3]));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
+                if (++st == S) st = 0, ph ^= 1u;
+            }
+            // the partial sums of the unit: [consumer][row of X][weight row]
+            mbar_wait_or_abort(&rempty[b], rph ^ 1u, abort);
+            float* pw = reinterpret_cast<float*>(smem + L.part() + b * L.part_stride()) + cw * a.mc * kDecPartPitch + g;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (m0 < sg.nr) {
+                    pw[m0 * kDecPartPitch + h * 16] = y[h][0];
+                    pw[m0 * kDecPartPitch + h * 16 + 8] = y[h][2];
+                }
+                if (m1 < sg.nr) {
+                    pw[m1 * kDecPartPitch + h * 16] = y[h][1];
+                    pw[m1 * kDecPartPitch + h * 16 + 8] = y[h][3];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rfull[b]);
+            if (++b == 2) b = 0, rph ^= 1u;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Rows of X at a time and stages that fit in `smem` bytes: as many rows as there are, up to 8, with
+// at least three stages.  false if not even one row fits.
+inline bool dec_plan(int rows, int K, int G, int smem, int& mc, int& S) {
+    for (mc = std::min(rows, kDecMaxRows); mc >= 1; --mc)
+        for (S = 6; S >= 3; --S)
+            if (DecSmem(mc, K, G, S).bytes() <= smem) return true;
+    return false;
+}
+
+inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d, int mc, int S, cudaStream_t st) {
+    CUtensorMap tq;
+    if (!make_tmap_3d(&tq, l.qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, 16, (uint64_t)l.E * l.N, (uint64_t)(l.K / 128),
+                      (uint64_t)l.K / 2, 64, 16, 16, kDecKC / 128))
+        return AWQ_ERR_CUDA;
+    const void* fn = l.G == 32    ? (const void*)linear_decode_kernel<32>
+                     : l.G == 64  ? (const void*)linear_decode_kernel<64>
+                     : l.G == 128 ? (const void*)linear_decode_kernel<128>
+                                  : (const void*)linear_decode_kernel<256>;
+    if (!prepare_kernel(fn)) return AWQ_ERR_CUDA;
+    DecArgs a = {l.X, l.ldx, l.scales, l.qzeros, l.rows, l.offsets, l.T, l.R, l.E, l.N, l.K, 0, mc, S, l.ep};
+    a.units = l.ep.gated ? ceil_div(l.N / 2, 16) : ceil_div(l.N, kDecRows);
+    // (grouped: every expert with rows adds at most one partial set)
+    const long long sets = l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc);
+    if (sets * a.units > 0x7fffffffLL) return AWQ_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)std::min<long long>(d.sms, sets * a.units));
+    lc.blockDim = dim3(kDecThreads);
+    lc.dynamicSmemBytes = DecSmem(mc, l.K, l.G, S).bytes();
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    void* args[] = {&tq, &a};
+    return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+// Which form takes a call.  The decode form reads the weights once per 8 rows of a matrix and needs
+// whole 128-code blocks; above that the tensor-core tiles win.
+inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaStream_t st) {
+    const int share = l.offsets ? ceil_div(l.R, std::min(l.R, l.E)) : l.R;
+    int mc = 0, S = 0;
+    if (share <= kDecMaxRows && l.K % 128 == 0 &&
+        dec_plan(l.offsets ? std::min(l.R, kDecMaxRows) : l.R, l.K, l.G, d.max_smem_optin, mc, S) && mc >= share)
+        return launch_linear_decode(l, d, mc, S, st);
+    return launch_linear_tc(l, d.sms, st);
+}
+
+}  // namespace awq
