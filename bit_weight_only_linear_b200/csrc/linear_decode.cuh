@@ -13,7 +13,7 @@
 //   * A persistent CTA per SM takes a contiguous range of units: all of one dense matrix, or the
 //     units of the experts that have rows (8 rows of an expert at a time), so that X is staged once
 //     per expert and CTA.
-//   * Warps: a producer (3-D TMA, 32 KB stages of 32 rows x 2048 codes), a converter (scales and
+//   * Warps: a producer (3-D TMA, 32 KB stages of 32 rows x 2048 codes), two converters (scales and
 //     zeros -> fp32 pairs per stage), 16 consumers (128 codes of a stage each), a reducer (the
 //     consumers' partial sums in a fixed order, then the epilogue).
 // K must be a multiple of 128.  Every wait is bounded.
@@ -29,7 +29,9 @@
 namespace awq {
 
 constexpr int kDecConsumers = 16;
-constexpr int kDecThreads = (3 + kDecConsumers) * 32;
+constexpr int kDecConverters = 2;
+constexpr int kDecReducer = 1 + kDecConverters, kDecConsumer0 = kDecReducer + 1;   // first warps of the roles
+constexpr int kDecThreads = (kDecConsumer0 + kDecConsumers) * 32;
 constexpr int kDecRows = 32;                     // weight rows per unit
 constexpr int kDecKC = 2048;                     // codes per row and stage
 constexpr int kDecStageBytes = kDecRows * kDecKC / 2;
@@ -105,6 +107,30 @@ __device__ __forceinline__ DecSeg dec_segment(const DecArgs& a, int u, int end) 
     return s;
 }
 
+// The stages of units u_begin .. u_end-1 in order, by a whole warp.
+struct DecIter {
+    int u, u_end, n, c, nchunks;
+    bool live;
+    DecSeg sg;
+    __device__ __forceinline__ DecIter(const DecArgs& a, int u_begin, int u_end_, int nchunks_)
+        : u(u_begin), u_end(u_end_), n(0), c(0), nchunks(nchunks_), live(u_begin < u_end_) {
+        if (live) open(a);
+    }
+    __device__ __forceinline__ void open(const DecArgs& a) {
+        sg = dec_segment(a, u, u_end);
+        u += sg.count;
+        n = sg.n;
+        c = 0;
+    }
+    __device__ __forceinline__ void next(const DecArgs& a) {
+        if (!live || ++c < nchunks) return;
+        c = 0;
+        if (++n < sg.n + sg.count) return;
+        live = u < u_end;
+        if (live) open(a);
+    }
+};
+
 template <int G>
 __global__ void __launch_bounds__(kDecThreads, 1)
 linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a) {
@@ -145,6 +171,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     const int u_begin = (int)(total * blockIdx.x / gridDim.x), u_end = (int)(total * (blockIdx.x + 1) / gridDim.x);
     const int nchunks = L.Kp / kDecKC;
     const int F = a.ep.gated ? a.N / 2 : a.N;
+    const uint32_t sbase = smem_u32(smem);
     // first rows of the two row tiles of unit n
     auto tile0 = [&](int n) { return a.ep.gated ? n * 16 : n * kDecRows; };
     auto tile1 = [&](int n) { return a.ep.gated ? F + n * 16 : n * kDecRows + 16; };
@@ -179,71 +206,85 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         for (int j = issued - 1; j >= 0 && j >= issued - S; --j) mbar_wait(&full[j % S], (j / S) & 1);
         return;
     }
-    if (warp == 1) {
-        // ---------------- converter: lane = row of the unit; scales and zero words of the next stage
-        // are fetched while the current one waits ----------------
+    if (warp < kDecReducer) {
+        // ---------------- converters: lane = row of the unit.  Each takes every second stage and holds
+        // the scales and zero words of the next kDepth of them in registers (a stage's loads take longer
+        // than the stage streams) ----------------
         constexpr int OCT = GPC / 8;                           // octets of groups per row and stage
+        constexpr int kDepth = OCT <= 4 ? 2 : 1;
         const int ng = a.K / G, nzw = ceil_div(ng, 8);
         const bool zp = a.qzeros != nullptr;
         const bool vec = (ng & 7) == 0;                        // 16-byte aligned scale rows
-        uint4 sc[OCT];
-        uint32_t zw[OCT];
-        auto fetch = [&](int expert, int n, int c) {
-            const int row = lane < 16 ? tile0(n) + lane : tile1(n) + lane - 16;
+        uint4 sc[kDepth][OCT];
+        uint32_t zw[kDepth][OCT];
+        auto fetch = [&](const DecIter& it, uint4 (&fs)[OCT], uint32_t (&fz)[OCT]) {
+            if (!it.live) return;
+            const int row = lane < 16 ? tile0(it.n) + lane : tile1(it.n) + lane - 16;
             const int lim = a.ep.gated && lane < 16 ? F : a.N;
-            const size_t wr = (size_t)expert * a.N + min(row, lim - 1);   // rows past the end: dropped later
+            const size_t wr = (size_t)it.sg.expert * a.N + min(row, lim - 1);   // rows past the end: dropped later
             const uint16_t* sp = a.scales + wr * ng;
 #pragma unroll
             for (int o = 0; o < OCT; ++o) {
-                const int g0 = c * GPC + 8 * o;
-                sc[o] = make_uint4(0u, 0u, 0u, 0u);                       // groups past K: scale 0
-                zw[o] = 0x88888888u;
+                const int g0 = it.c * GPC + 8 * o;
+                fs[o] = make_uint4(0u, 0u, 0u, 0u);                             // groups past K: scale 0
+                fz[o] = 0x88888888u;
                 if (g0 < ng) {
                     if (vec) {
-                        sc[o] = __ldg(reinterpret_cast<const uint4*>(sp + g0));
+                        fs[o] = __ldg(reinterpret_cast<const uint4*>(sp + g0));
                     } else {
                         uint32_t h[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) h[i] = g0 + i < ng ? __ldg(sp + g0 + i) : 0u;
-                        sc[o] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                        fs[o] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
                     }
-                    if (zp) zw[o] = __ldg(a.qzeros + wr * nzw + (g0 >> 3));
+                    if (zp) fz[o] = __ldg(a.qzeros + wr * nzw + (g0 >> 3));
                 }
             }
         };
-        int st = 0;
+        DecIter fetched(a, u_begin, u_end, nchunks);          // the next stage to fetch
+        if (warp == 2) fetched.next(a);
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            fetch(fetched, sc[d], zw[d]);
+            fetched.next(a);
+            fetched.next(a);
+        }
+        const int stages = (u_end - u_begin) * nchunks;
+        int st = warp - 1;
         uint32_t ph = 0;
-        for (int u = u_begin; u < u_end;) {
-            const DecSeg sg = dec_segment(a, u, u_end);
-            u += sg.count;
-            fetch(sg.expert, sg.n, 0);
-            for (int n = sg.n; n < sg.n + sg.count; ++n) {
-                for (int c = 0; c < nchunks; ++c) {
-                    mbar_wait_or_abort(&empty[st], ph ^ 1u, abort);
-                    float4* dst = reinterpret_cast<float4*>(smem + L.cvt() + (st * kDecRows + lane) * L.cvt_pitch());
+        for (int i = warp - 1; i < stages;) {
 #pragma unroll
-                    for (int o = 0; o < OCT; ++o) {
-                        const uint32_t hw[4] = {sc[o].x, sc[o].y, sc[o].z, sc[o].w};
+            for (int d = 0; d < kDepth; ++d) {
+                if (i >= stages) break;
+                mbar_wait_or_abort(&empty[st], ph ^ 1u, abort);
+                float4* dst = reinterpret_cast<float4*>(smem + L.cvt() + (st * kDecRows + lane) * L.cvt_pitch());
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float s0 = h2f((uint16_t)(hw[k] & 0xFFFFu)), s1 = h2f((uint16_t)(hw[k] >> 16));
-                            const float z0 = (float)((zw[o] >> (8 * k)) & 15u), z1 = (float)((zw[o] >> (8 * k + 4)) & 15u);
-                            dst[o * 4 + k] = make_float4(s0 * 16777216.0f, s0 * z0, s1 * 16777216.0f, s1 * z1);
-                        }
+                for (int o = 0; o < OCT; ++o) {
+                    const uint32_t hw[4] = {sc[d][o].x, sc[d][o].y, sc[d][o].z, sc[d][o].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float s0 = h2f((uint16_t)(hw[k] & 0xFFFFu)), s1 = h2f((uint16_t)(hw[k] >> 16));
+                        const float z0 = (float)((zw[d][o] >> (8 * k)) & 15u), z1 = (float)((zw[d][o] >> (8 * k + 4)) & 15u);
+                        dst[o * 4 + k] = make_float4(s0 * 16777216.0f, s0 * z0, s1 * 16777216.0f, s1 * z1);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[st]);
-                    if (++st == S) st = 0, ph ^= 1u;
-                    if (c + 1 < nchunks) fetch(sg.expert, n, c + 1);
-                    else if (n + 1 < sg.n + sg.count) fetch(sg.expert, n + 1, 0);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[st]);
+                st += kDecConverters;
+                if (st >= S) st -= S, ph ^= 1u;
+                i += kDecConverters;
+                fetch(fetched, sc[d], zw[d]);
+                fetched.next(a);
+                fetched.next(a);
             }
         }
         return;
     }
-    if (warp == 2) {
-        // ---------------- reducer: lane = row of the unit; the consumers' sums in order, the epilogue ----------------
+    if (warp == kDecReducer) {
+        // ---------------- reducer: the consumers' sums in order, then the epilogue.  Lane = (row of X,
+        // four weight rows), two rows of X a lane; 16-byte reads, all independent ----------------
         const Epilogue& ep = a.ep;
+        const int quad = lane & 7;
         int b = 0;
         uint32_t ph = 0;
         for (int u = u_begin; u < u_end;) {
@@ -251,25 +292,47 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
             u += sg.count;
             const uint16_t* bias = ep.bias ? ep.bias + (size_t)sg.expert * a.N : nullptr;
             for (int n = sg.n; n < sg.n + sg.count; ++n) {
-                const int row = lane < 16 ? tile0(n) + lane : tile1(n) + lane - 16;
-                const int lim = ep.gated && lane < 16 ? F : a.N;
-                const float bv = bias && row < lim ? h2f(__ldg(bias + row)) : 0.0f;
-                const bool store = row < lim && (!ep.gated || lane < 16);
+                const int row = quad < 4 ? tile0(n) + quad * 4 : tile1(n) + quad * 4 - 16;
+                const int lim = ep.gated && quad < 4 ? F : a.N;
+                float bv[4] = {};
+                if (bias) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (row + i < lim) bv[i] = h2f(__ldg(bias + row + i));
+                }
                 mbar_wait_or_abort(&rfull[b], ph, abort);
                 __syncwarp();
-                const float* slot = reinterpret_cast<const float*>(smem + L.part() + b * L.part_stride()) + lane;
-                for (int m = 0; m < sg.nr; ++m) {
-                    float res = 0.0f;
-                    if (ep.residual && store) res = h2f(ep.residual[(size_t)(sg.r0 + m) * ep.ldr + row]);
-                    float acc = 0.0f;
+                const uint32_t slot = sbase + (uint32_t)(L.part() + b * L.part_stride() + quad * 16);
 #pragma unroll
-                    for (int w = 0; w < kDecConsumers; ++w) acc += slot[(w * a.mc + m) * kDecPartPitch];
-                    acc += bv;
-                    const float other = __shfl_down_sync(0xffffffffu, acc, 16);
-                    float y[1] = {acc};
+                for (int it = 0; it < 2; ++it) {
+                    if (it * 4 >= sg.nr) break;
+                    const int m = it * 4 + (lane >> 3), mm = min(m, sg.nr - 1);
+                    const bool store = m < sg.nr && (!ep.gated || quad < 4);
+                    float y[4] = {}, res[4] = {};
+                    if (ep.residual && store) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (row + i < lim) res[i] = h2f(ep.residual[(size_t)(sg.r0 + m) * ep.ldr + row + i]);
+                    }
+#pragma unroll
+                    for (int w = 0; w < kDecConsumers; ++w) {
+                        const uint4 v = lds128(slot + (uint32_t)((w * a.mc + mm) * kDecPartPitch * 4));
+                        y[0] += __uint_as_float(v.x), y[1] += __uint_as_float(v.y);
+                        y[2] += __uint_as_float(v.z), y[3] += __uint_as_float(v.w);
+                    }
+                    float other[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] += bv[i];
+                        other[i] = __shfl_down_sync(0xffffffffu, y[i], 4);
+                    }
                     apply_act(y, ep.act);
-                    if (ep.gated) y[0] *= other;
-                    if (store) ep.Y[(size_t)(sg.r0 + m) * ep.ldy + row] = f2h_rn(y[0] + res);
+                    uint16_t* yp = ep.Y + (size_t)(sg.r0 + m) * ep.ldy + row;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (ep.gated) y[i] *= other[i];
+                        if (store && row + i < lim) yp[i] = f2h_rn(y[i] + res[i]);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rempty[b]);
@@ -283,12 +346,11 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     constexpr int kCons = kDecConsumers * 32;
     constexpr int R = G >= kStepCodes ? G / kStepCodes : 1;     // k-steps per group
     constexpr int TPS = 4 * WT;                                  // 16-byte chunks per k-step
-    const int cw = warp - 3, ct = threadIdx.x - 96;
+    const int cw = warp - kDecConsumer0, ct = threadIdx.x - kDecConsumer0 * 32;
     const int g = lane >> 2, t = lane & 3;
     const int pitch = L.x_pitch();
     uint8_t* xs = smem + L.x();
     float* xsum = reinterpret_cast<float*>(smem + L.xsum());
-    const uint32_t sbase = smem_u32(smem);
     // weights: row r of a tile, block b of 128 codes: [b][r][64 bytes]; this warp's block is cw
     const uint32_t wofs = (uint32_t)(cw * 1024 + g * 64 + t * WT * 4);
     const uint32_t cofs = smem_u32(smem + L.cvt()) + (uint32_t)(g * L.cvt_pitch() + (cw * 128 / G) * 8);
@@ -305,18 +367,25 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory");       // the previous segment's X is done with
         {
             const int kwp = L.Kp >> 3, kwv = a.K >> 3;                 // kwp is a multiple of 256
-            for (int m = 0; m < sg.nr; ++m) {
-                int src = sg.r0 + m;
-                if (a.rows) src = __ldg(a.rows + src);
-                const bool live = src >= 0 && src < a.T;
-                const uint4* row = reinterpret_cast<const uint4*>(a.X + (live ? src : 0) * a.ldx);
-                uint4* dst = reinterpret_cast<uint4*>(xs + m * pitch);
-                for (int word = ct; word < kwp; word += kCons) {
-                    const uint4 v = live && word < kwv ? __ldg(row + word) : make_uint4(0u, 0u, 0u, 0u);
-                    const int s = word / TPS, r = word % TPS;
-                    const int tt = r / WT, j = r % WT;
-                    dst[(s * WT + j) * 4 + tt] = make_uint4(v.x, v.z, v.y, v.w);
-                    const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+            int src[kDecMaxRows];
+#pragma unroll
+            for (int m = 0; m < kDecMaxRows; ++m) {
+                src[m] = m < sg.nr ? (a.rows ? __ldg(a.rows + sg.r0 + m) : sg.r0 + m) : -1;
+                if (src[m] >= a.T) src[m] = -1;
+            }
+            for (int word = ct; word < kwp; word += kCons) {
+                const int s = word / TPS, r = word % TPS;
+                const int tt = r / WT, j = r % WT;
+                uint4 v[kDecMaxRows];                                  // every row's load before the first use
+#pragma unroll
+                for (int m = 0; m < kDecMaxRows; ++m)
+                    v[m] = src[m] >= 0 && word < kwv ? __ldg(reinterpret_cast<const uint4*>(a.X + src[m] * a.ldx) + word)
+                                                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int m = 0; m < kDecMaxRows; ++m) {
+                    if (m >= sg.nr) break;
+                    reinterpret_cast<uint4*>(xs + m * pitch)[(s * WT + j) * 4 + tt] = make_uint4(v[m].x, v[m].z, v[m].y, v[m].w);
+                    const uint16_t* h = reinterpret_cast<const uint16_t*>(&v[m]);
                     float acc = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) acc += h2f(h[e]);
