@@ -36,6 +36,7 @@ constexpr int kDecRows = 32;                     // weight rows per unit
 constexpr int kDecKC = 2048;                     // codes per row and stage
 constexpr int kDecStageBytes = kDecRows * kDecKC / 2;
 constexpr int kDecMaxRows = 8;                   // rows of X at a time (MMA N)
+constexpr int kDecMaxSegs = 32;                  // segments of a CTA
 constexpr int kDecPartPitch = 36;                // words per row of X in a partial sum (bank spread)
 
 struct DecSmem {
@@ -54,8 +55,9 @@ struct DecSmem {
     __host__ __device__ int part() const { return (xsum() + M * nsteps * 4 + 15) & ~15; }
     __host__ __device__ int part_stride() const { return kDecConsumers * M * kDecPartPitch * 4; }
     __host__ __device__ int bars() const { return part() + 2 * part_stride(); }
-    // full[S], empty[S], rfull[2], rempty[2]
-    __host__ __device__ int bytes() const { return bars() + (2 * S + 4) * 8 + 128; }
+    // full[S], empty[S], rfull[2], rempty[2], abort flag and segment count, segments
+    __host__ __device__ int segs() const { return bars() + (2 * S + 4) * 8 + 8; }
+    __host__ __device__ int bytes() const { return segs() + kDecMaxSegs * 20; }
 };
 
 struct DecArgs {
@@ -107,27 +109,20 @@ __device__ __forceinline__ DecSeg dec_segment(const DecArgs& a, int u, int end) 
     return s;
 }
 
-// The stages of units u_begin .. u_end-1 in order, by a whole warp.
+// The stages of a CTA's segments in order.
 struct DecIter {
-    int u, u_end, n, c, nchunks;
-    bool live;
-    DecSeg sg;
-    __device__ __forceinline__ DecIter(const DecArgs& a, int u_begin, int u_end_, int nchunks_)
-        : u(u_begin), u_end(u_end_), n(0), c(0), nchunks(nchunks_), live(u_begin < u_end_) {
-        if (live) open(a);
+    const DecSeg *sg, *end;
+    int n, c, nchunks;
+    __device__ __forceinline__ DecIter(const DecSeg* segs, int count, int nchunks_)
+        : sg(segs), end(segs + count), n(0), c(0), nchunks(nchunks_) {
+        if (live()) n = sg->n;
     }
-    __device__ __forceinline__ void open(const DecArgs& a) {
-        sg = dec_segment(a, u, u_end);
-        u += sg.count;
-        n = sg.n;
+    __device__ __forceinline__ bool live() const { return sg < end; }
+    __device__ __forceinline__ void next() {
+        if (!live() || ++c < nchunks) return;
         c = 0;
-    }
-    __device__ __forceinline__ void next(const DecArgs& a) {
-        if (!live || ++c < nchunks) return;
-        c = 0;
-        if (++n < sg.n + sg.count) return;
-        live = u < u_end;
-        if (live) open(a);
+        if (++n < sg->n + sg->count) return;
+        if (++sg < end) n = sg->n;
     }
 };
 
@@ -163,12 +158,24 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         prefetch_tensormap(&tmap_q);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Grouped, the table decides which weights are read; dense, the weights stream before the previous
+    // kernel has completed, and only X, the residual and Y wait for it (below).
+    if (a.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
+    DecSeg* segs = reinterpret_cast<DecSeg*>(smem + L.segs());
+    if (warp == 1) {
+        // this CTA's share of all row sets' units, as segments
+        const long long total = (long long)dec_sets(a) * a.units;
+        const int u_begin = (int)(total * blockIdx.x / gridDim.x), u_end = (int)(total * (blockIdx.x + 1) / gridDim.x);
+        int count = 0;
+        for (int u = u_begin; u < u_end && count < kDecMaxSegs; ++count) {
+            const DecSeg sg = dec_segment(a, u, u_end);
+            if (lane == 0) segs[count] = sg;
+            u += sg.count;
+        }
+        if (lane == 0) abort[1] = (uint32_t)count;
+    }
     __syncthreads();
-
-    // this CTA's units, of all row sets' units
-    const long long total = (long long)dec_sets(a) * a.units;
-    const int u_begin = (int)(total * blockIdx.x / gridDim.x), u_end = (int)(total * (blockIdx.x + 1) / gridDim.x);
+    const int nseg = (int)abort[1];
     const int nchunks = L.Kp / kDecKC;
     const int F = a.ep.gated ? a.N / 2 : a.N;
     const uint32_t sbase = smem_u32(smem);
@@ -181,9 +188,8 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         int st = 0, issued = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = u_begin; u < u_end && ok;) {
-            const DecSeg sg = dec_segment(a, u, u_end);
-            u += sg.count;
+        for (int i = 0; i < nseg && ok; ++i) {
+            const DecSeg sg = segs[i];
             for (int n = sg.n; n < sg.n + sg.count && ok; ++n) {
                 const int ra = sg.expert * a.N + tile0(n), rb = sg.expert * a.N + tile1(n);
                 for (int c = 0; c < nchunks; ++c) {
@@ -218,10 +224,10 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         uint4 sc[kDepth][OCT];
         uint32_t zw[kDepth][OCT];
         auto fetch = [&](const DecIter& it, uint4 (&fs)[OCT], uint32_t (&fz)[OCT]) {
-            if (!it.live) return;
+            if (!it.live()) return;
             const int row = lane < 16 ? tile0(it.n) + lane : tile1(it.n) + lane - 16;
             const int lim = a.ep.gated && lane < 16 ? F : a.N;
-            const size_t wr = (size_t)it.sg.expert * a.N + min(row, lim - 1);   // rows past the end: dropped later
+            const size_t wr = (size_t)it.sg->expert * a.N + min(row, lim - 1);   // rows past the end: dropped later
             const uint16_t* sp = a.scales + wr * ng;
 #pragma unroll
             for (int o = 0; o < OCT; ++o) {
@@ -241,21 +247,21 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
                 }
             }
         };
-        DecIter fetched(a, u_begin, u_end, nchunks);          // the next stage to fetch
-        if (warp == 2) fetched.next(a);
+        DecIter fetched(segs, nseg, nchunks);                 // the next stage to fetch
+        DecIter it(segs, nseg, nchunks);                      // the next to convert
+        if (warp == 2) fetched.next(), it.next();
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             fetch(fetched, sc[d], zw[d]);
-            fetched.next(a);
-            fetched.next(a);
+            fetched.next();
+            fetched.next();
         }
-        const int stages = (u_end - u_begin) * nchunks;
         int st = warp - 1;
         uint32_t ph = 0;
-        for (int i = warp - 1; i < stages;) {
+        while (it.live()) {
 #pragma unroll
             for (int d = 0; d < kDepth; ++d) {
-                if (i >= stages) break;
+                if (!it.live()) break;
                 mbar_wait_or_abort(&empty[st], ph ^ 1u, abort);
                 float4* dst = reinterpret_cast<float4*>(smem + L.cvt() + (st * kDecRows + lane) * L.cvt_pitch());
 #pragma unroll
@@ -272,10 +278,11 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
                 if (lane == 0) mbar_arrive(&full[st]);
                 st += kDecConverters;
                 if (st >= S) st -= S, ph ^= 1u;
-                i += kDecConverters;
+                it.next();
+                it.next();
                 fetch(fetched, sc[d], zw[d]);
-                fetched.next(a);
-                fetched.next(a);
+                fetched.next();
+                fetched.next();
             }
         }
         return;
@@ -283,13 +290,13 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     if (warp == kDecReducer) {
         // ---------------- reducer: the consumers' sums in order, then the epilogue.  Lane = (row of X,
         // four weight rows), two rows of X a lane; 16-byte reads, all independent ----------------
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         const Epilogue& ep = a.ep;
         const int quad = lane & 7;
         int b = 0;
         uint32_t ph = 0;
-        for (int u = u_begin; u < u_end;) {
-            const DecSeg sg = dec_segment(a, u, u_end);
-            u += sg.count;
+        for (int i = 0; i < nseg; ++i) {
+            const DecSeg sg = segs[i];
             const uint16_t* bias = ep.bias ? ep.bias + (size_t)sg.expert * a.N : nullptr;
             for (int n = sg.n; n < sg.n + sg.count; ++n) {
                 const int row = quad < 4 ? tile0(n) + quad * 4 : tile1(n) + quad * 4 - 16;
@@ -358,40 +365,47 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     const int m0 = 2 * t, m1 = 2 * t + 1;
     int st = 0, b = 0;
     uint32_t ph = 0, rph = 0;
-    for (int u = u_begin; u < u_end;) {
-        const DecSeg sg = dec_segment(a, u, u_end);
-        u += sg.count;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = 0; i < nseg; ++i) {
+        const DecSeg sg = segs[i];
         // X of the segment: 16-byte chunks reordered within each k-step to [j][t] with the middle words
         // swapped (so that a fragment is a register pair of one 16-byte read), zeros past K and for rows
         // that do not exist; per-k-step sums of x
         asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory");       // the previous segment's X is done with
         {
             const int kwp = L.Kp >> 3, kwv = a.K >> 3;                 // kwp is a multiple of 256
-            int src[kDecMaxRows];
+            constexpr int kBatch = 4;                                  // rows whose loads are in flight together
+#pragma unroll 1
+            for (int mb = 0; mb < sg.nr; mb += kBatch) {
+                const uint4* row[kBatch];
 #pragma unroll
-            for (int m = 0; m < kDecMaxRows; ++m) {
-                src[m] = m < sg.nr ? (a.rows ? __ldg(a.rows + sg.r0 + m) : sg.r0 + m) : -1;
-                if (src[m] >= a.T) src[m] = -1;
-            }
-            for (int word = ct; word < kwp; word += kCons) {
-                const int s = word / TPS, r = word % TPS;
-                const int tt = r / WT, j = r % WT;
-                uint4 v[kDecMaxRows];                                  // every row's load before the first use
+                for (int i = 0; i < kBatch; ++i) {
+                    int src = -1;
+                    if (mb + i < sg.nr) src = a.rows ? __ldg(a.rows + sg.r0 + mb + i) : sg.r0 + mb + i;
+                    row[i] = src >= 0 && src < a.T ? reinterpret_cast<const uint4*>(a.X + src * a.ldx) : nullptr;
+                }
+#pragma unroll 1
+                for (int word = ct; word < kwp; word += kCons) {
+                    const int s = word / TPS, r = word % TPS;
+                    const int tt = r / WT, j = r % WT;
+                    uint4 v[kBatch];
 #pragma unroll
-                for (int m = 0; m < kDecMaxRows; ++m)
-                    v[m] = src[m] >= 0 && word < kwv ? __ldg(reinterpret_cast<const uint4*>(a.X + src[m] * a.ldx) + word)
-                                                     : make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = 0; i < kBatch; ++i)
+                        v[i] = row[i] && word < kwv ? __ldg(row[i] + word) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int m = 0; m < kDecMaxRows; ++m) {
-                    if (m >= sg.nr) break;
-                    reinterpret_cast<uint4*>(xs + m * pitch)[(s * WT + j) * 4 + tt] = make_uint4(v[m].x, v[m].z, v[m].y, v[m].w);
-                    const uint16_t* h = reinterpret_cast<const uint16_t*>(&v[m]);
-                    float acc = 0.0f;
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int m = mb + i;
+                        if (m >= sg.nr) break;
+                        reinterpret_cast<uint4*>(xs + m * pitch)[(s * WT + j) * 4 + tt] =
+                            make_uint4(v[i].x, v[i].z, v[i].y, v[i].w);
+                        const uint16_t* h = reinterpret_cast<const uint16_t*>(&v[i]);
+                        float acc = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc += h2f(h[e]);
+                        for (int e = 0; e < 8; ++e) acc += h2f(h[e]);
 #pragma unroll
-                    for (int o = TPS / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-                    if (r == 0) xsum[m * L.nsteps + s] = acc;
+                        for (int o = TPS / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                        if (r == 0) xsum[m * L.nsteps + s] = acc;
+                    }
                 }
             }
         }
@@ -504,9 +518,9 @@ inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d,
     a.units = l.ep.gated ? ceil_div(l.N / 2, 16) : ceil_div(l.N, kDecRows);
     // (grouped: every expert with rows adds at most one partial set)
     const long long sets = l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc);
-    if (sets * a.units > 0x7fffffffLL) return AWQ_ERR_UNSUPPORTED;
+    const long long grid = std::min<long long>(d.sms, sets * a.units);
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)std::min<long long>(d.sms, sets * a.units));
+    lc.gridDim = dim3((unsigned)grid);
     lc.blockDim = dim3(kDecThreads);
     lc.dynamicSmemBytes = DecSmem(mc, l.K, l.G, S).bytes();
     lc.stream = st;
@@ -524,9 +538,12 @@ inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d,
 inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaStream_t st) {
     const int share = l.offsets ? ceil_div(l.R, std::min(l.R, l.E)) : l.R;
     int mc = 0, S = 0;
-    if (share <= kDecMaxRows && l.K % 128 == 0 &&
-        dec_plan(l.offsets ? std::min(l.R, kDecMaxRows) : l.R, l.K, l.G, d.max_smem_optin, mc, S) && mc >= share)
-        return launch_linear_decode(l, d, mc, S, st);
+    if (share <= kDecMaxRows && l.K % 128 == 0 && dec_plan(l.R, l.K, l.G, d.max_smem_optin, mc, S) && mc >= share) {
+        // a CTA's list of segments must hold the row sets that its units may reach
+        const long long sets = l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc);
+        if (sets <= (long long)(kDecMaxSegs - 2) * d.sms && sets * ceil_div(l.N, 32) < 0x7fffffffLL)
+            return launch_linear_decode(l, d, mc, S, st);
+    }
     return launch_linear_tc(l, d.sms, st);
 }
 
