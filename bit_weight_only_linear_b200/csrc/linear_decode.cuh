@@ -97,10 +97,10 @@ __device__ __forceinline__ DecSeg dec_segment(const DecArgs& a, int u, int end) 
     s.n = u - set * a.units;
     s.count = min(a.units - s.n, end - u);
     if (a.offsets) {
-        const int4 t = find_tile(a.offsets, a.E, a.R, a.mc, 1, set);
+        const int4 t = find_tile(a.offsets, a.E, a.R, a.mc, 1, 1, set);
         s.expert = t.x;
         s.r0 = t.y;
-        s.nr = min(a.mc, t.z - t.y);
+        s.nr = t.z - t.y;
     } else {
         s.expert = 0;
         s.r0 = set * a.mc;

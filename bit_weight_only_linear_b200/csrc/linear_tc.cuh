@@ -75,16 +75,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// fp32 at the shared-memory address `a` of this CTA, in CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_cluster(uint32_t a, uint32_t rank) {
-    float v;
-    asm volatile("{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
-                 : "=f"(v)
-                 : "r"(a), "r"(rank)
-                 : "memory");
+// Four fp32 at the shared-memory address `a` of this CTA, in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, "
+        "[r];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(a), "r"(rank)
+        : "memory");
     return v;
 }
 
+constexpr int kTcMaxSplits = 8;          // CTAs of a cluster that share a tile's K
 constexpr int kTcRows = 256;             // weight rows per tile: two MMA row tiles
 constexpr int kTcWKB = 4;                // k-blocks (64 codes) per packed stage: 128-byte lines
 
@@ -136,11 +139,17 @@ __device__ __forceinline__ int2 expert_range(const int32_t* offsets, int e, int 
     return make_int2(b, min(max(__ldg(offsets + e + 1), b), R));
 }
 
-// The `tile`-th row tile of the experts' ranges, each cut into tiles of `bn` rows: {expert, first
-// row, end of the expert's rows}, expert -1 if there are fewer tiles.  By a whole warp.  `per`
-// consecutive tile numbers belong to each row tile (its tiles of weight rows); the caller gets the
-// remainder in `sub`, with the row tiles of an expert innermost.
-__device__ __forceinline__ int4 find_tile(const int32_t* offsets, int E, int R, int bn, int per, long long tile) {
+// Rows of each of the tiles of at most `bn` rows that `m` rows are cut into: even shares, in steps
+// of `step` (a divisor of bn).
+__device__ __forceinline__ int tile_rows(int m, int tiles, int step) {
+    return ((m + tiles - 1) / tiles + step - 1) / step * step;
+}
+
+// The `tile`-th tile of the experts' ranges: {expert, first row, end of the tile's rows, tile of weight
+// rows}, expert -1 if there are fewer tiles.  By a whole warp.  Each expert has ceil(rows / bn) row
+// tiles by `per` tiles of weight rows, the row tiles innermost.
+__device__ __forceinline__ int4 find_tile(const int32_t* offsets, int E, int R, int bn, int step, int per,
+                                          long long tile) {
     const int lane = threadIdx.x & 31;
     for (int e0 = 0; e0 < E; e0 += 32) {
         const int e = e0 + lane;
@@ -159,7 +168,8 @@ __device__ __forceinline__ int4 find_tile(const int32_t* offsets, int E, int R, 
             const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
             const int in = (int)(tile - (x - v));          // tile inside the expert
             const int m = mt ? in % mt : 0, n = mt ? in / mt : 0;
-            int4 r = make_int4(e, g.x + m * bn, g.y, n);
+            const int rows = mt ? tile_rows(g.y - g.x, mt, step) : 0;
+            int4 r = make_int4(e, g.x + m * rows, min(g.y, g.x + (m + 1) * rows), n);
             r.x = __shfl_sync(0xffffffffu, r.x, src);
             r.y = __shfl_sync(0xffffffffu, r.y, src);
             r.z = __shfl_sync(0xffffffffu, r.z, src);
@@ -225,9 +235,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         // the CTA's tile and the rows of X that it reads
         int4 t;
         if (a.offsets)
-            t = find_tile(a.offsets, a.E, a.R, BN, a.n_tiles, tile);
-        else
-            t = make_int4(0, (tile % a.m_tiles) * BN, a.R, tile / a.m_tiles);
+            t = find_tile(a.offsets, a.E, a.R, BN, 16, a.n_tiles, tile);
+        else {
+            const int rows = tile_rows(a.R, a.m_tiles, 16), r0 = (tile % a.m_tiles) * rows;
+            t = make_int4(0, r0, min(a.R, r0 + rows), tile / a.m_tiles);
+        }
+        if (t.y >= t.z) t.x = -1;
         if (lane == 0) {
             misc[1] = (uint32_t)t.x;
             misc[2] = (uint32_t)t.y;
@@ -332,7 +345,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     } else if (warp == C::kMmaWarp) {
         if (elect_one()) {
             // ---------------- MMA issuer ----------------
-            constexpr uint32_t idesc = idesc_f16_f32(128, BN);
+            const uint32_t idesc = idesc_f16_f32(128, (r1 - r0 + 15) & ~15);    // as many columns as there are rows
             const uint64_t bdesc0 = desc_sw128_kmajor(smem_u32(smem + C::kXOff));
             int s = 0, b = 0;
             uint32_t xph = 0, aph = 0;
@@ -508,7 +521,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             constexpr int cw = BN * 2 / kSets;
             constexpr int CH = cw < 16 ? 8 : 16;
             const int c0 = (set >> 1) * cw;
-            for (int c = c0; c < c0 + cw; c += CH) {
+            for (int c = c0; c < c0 + cw && r0 + c < r1; c += CH) {
                 uint32_t u[CH];
                 if constexpr (CH == 16) tmem_ld16(acc0 + h * BN + lanes + (uint32_t)c, u);
                 else tmem_ld8(acc0 + h * BN + lanes + (uint32_t)c, u);
@@ -525,30 +538,48 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     if (splits > 1) {
         __syncwarp();
         cluster_sync_all();
-        // rank's share of the outputs: columns rank, rank + splits, ..; the partial sums in rank order
-        const float* part = reinterpret_cast<const float*>(smem);
-        const uint32_t base = smem_u32(part);
+        // rank's share of the outputs: columns rank, rank + splits, ..; a thread takes four weight rows of a
+        // column and adds the partial sums in rank order, all reads under way at once
+        const uint32_t base = smem_u32(smem);
         const Epilogue& ep = a.ep;
-        const int per_col = ep.gated ? 128 : kTcRows;
-        const int cols = expert < 0 ? 0 : min(BN, r1 - r0);
+        const int quads = ep.gated ? 32 : kTcRows / 4;
+        const int cols = expert < 0 ? 0 : r1 - r0;
         const int mine = cols > (int)rank ? (cols - 1 - (int)rank) / (int)splits + 1 : 0;
         const uint16_t* bias = ep.bias ? ep.bias + (size_t)max(expert, 0) * a.N : nullptr;
-        for (int i = threadIdx.x; i < mine * per_col; i += C::kThreads) {
-            const int c = (int)rank + (i / per_col) * (int)splits, l = i % per_col;
+        for (int i = threadIdx.x; i < mine * quads; i += C::kThreads) {
+            const int c = (int)rank + (i / quads) * (int)splits, l = (i % quads) * 4;
             const int nn = n0 + l;                 // (not gated: n1 = n0 + 128)
             if (nn >= F) continue;
-            const int m = r0 + c;
-            const uint32_t at = base + (uint32_t)(c * kTcRows + l) * 4;
-            float v0 = 0.0f, v1 = 0.0f;
-            for (uint32_t s = 0; s < splits; ++s) {
-                v0 += ld_cluster(at, s);
-                if (ep.gated) v1 += ld_cluster(at + 512, s);
+            const size_t m = r0 + c;
+            float v[2][4] = {};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h && !ep.gated) break;
+                const uint32_t at = base + (uint32_t)(c * kTcRows + h * 128 + l) * 4;
+                float4 p[kTcMaxSplits];
+#pragma unroll
+                for (int s = 0; s < kTcMaxSplits; ++s)
+                    if (s < (int)splits) p[s] = ld_cluster4(at, (uint32_t)s);
+#pragma unroll
+                for (int s = 0; s < kTcMaxSplits; ++s)
+                    if (s < (int)splits) v[h][0] += p[s].x, v[h][1] += p[s].y, v[h][2] += p[s].z, v[h][3] += p[s].w;
             }
-            float y[1] = {v0 + (bias ? h2f(bias[nn]) : 0.0f)};
-            apply_act(y, ep.act);
-            if (ep.gated) y[0] *= v1 + (bias ? h2f(bias[F + nn]) : 0.0f);
-            if (ep.residual) y[0] += h2f(ep.residual[(size_t)m * ep.ldr + nn]);
-            ep.Y[(size_t)m * ep.ldy + nn] = f2h_rn(y[0]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (bias && nn + j < F) {
+                    v[0][j] += h2f(bias[nn + j]);
+                    if (ep.gated) v[1][j] += h2f(bias[F + nn + j]);
+                }
+            apply_act(v[0], ep.act);
+            uint16_t* yp = ep.Y + m * ep.ldy + nn;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (nn + j >= F) break;
+                float y = v[0][j];
+                if (ep.gated) y *= v[1][j];
+                if (ep.residual) y += h2f(ep.residual[m * ep.ldr + nn + j]);
+                yp[j] = f2h_rn(y);
+            }
         }
         __syncwarp();
         cluster_sync_all();     // no CTA leaves while another reads its shared memory
@@ -636,7 +667,7 @@ awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
 // at least half of the slots idle and a split keeps two packed stages (512 codes).
 inline int tc_splits(long long tiles, int slots, int K) {
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= slots && ceil_div(K, kGemmKB * kTcWKB) >= 4 * s) s *= 2;
+    while (s < kTcMaxSplits && tiles * s * 2 <= slots && ceil_div(K, kGemmKB * kTcWKB) >= 4 * s) s *= 2;
     return s;
 }
 
