@@ -101,8 +101,8 @@ struct TcCfg {
     static constexpr int kMmaWarp = kXWarps, kWWarp = kXWarps + 1, kDqWarp0 = kXWarps + 2;
     static constexpr int kThreads = 32 * (kDqWarp0 + kDqWarps);
     static constexpr uint32_t kTmemCols = 512 / kCtas;
-    static constexpr int kABufs = BN <= 32 ? 3 : (BN == 128 ? 4 : 2);      // x 64 columns (two tiles x 64 codes)
-    static constexpr int kXStages = BN == 192 ? 5 : (BN == 128 ? 6 : (BN == 64 ? 5 : (BN == 32 ? 8 : 4)));
+    static constexpr int kABufs = BN == 128 ? 4 : 2;      // x 64 columns (two tiles x 64 codes); divides kTcWKB
+    static constexpr int kXStages = BN == 192 ? 5 : (BN == 128 ? 6 : (BN == 64 ? 5 : (BN == 32 ? 10 : 6)));
     static constexpr int kWStages = BN == 64 || BN == 32 ? 2 : 3;
     static constexpr int kXBytes = BN * 128;
     static constexpr int kWBytes = kTcRows * 32 * kTcWKB;
@@ -126,7 +126,7 @@ struct TcArgs {
     const uint32_t* qzeros;              // NULL: implicit zero 8
     const int32_t* rows;                 // row numbers of X, or NULL
     const int32_t* offsets;              // [E+1], or NULL: one range of R rows
-    int T, R, E, N, K, G;
+    int T, R, E, N, K;
     int n_tiles;                         // tiles of weight rows
     int m_tiles;                         // tiles of X rows (dense)
     int kb_per;                          // k-blocks per split (a multiple of kTcWKB)
@@ -181,7 +181,7 @@ __device__ __forceinline__ int4 find_tile(const int32_t* offsets, int E, int R, 
     return make_int4(-1, 0, 0, 0);
 }
 
-template <int BN>
+template <int BN, int G>
 __global__ void __launch_bounds__(TcCfg<BN>::kThreads, TcCfg<BN>::kCtas)
 linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_q,
                  const TcArgs a) {
@@ -378,58 +378,85 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         const int r = q * 32 + lane;
         const int n = (h ? n1 : n0) + r;
         const bool row_ok = n < (h ? end1 : end0);
-        const int ng = a.K / a.G;
+        const int ng = a.K / G;
         const int nzw = ceil_div(ng, 8);
         const bool zp = a.qzeros != nullptr;
-        const int lg = 31 - __clz(a.G);           // G is a power of two
         const size_t wrow = (size_t)max(expert, 0) * a.N + (row_ok ? n : 0);
         const uint16_t* srow = a.scales + wrow * ng;
         const uint32_t* zrow = a.qzeros + wrow * nzw;
-        // the next group's scale and zero word are fetched a group ahead of their use
-        int k = kb0 * kGemmKB + part0 * 32;
-        const int gstep = max(1, (kParts == 1 ? kGemmKB : 32) >> lg);   // groups between a thread's parts
-        uint32_t sc_next = 0, zw_next = 0;
-        if (k < a.K && num_kb > 0) {
-            sc_next = __ldg(srow + (k >> lg));
-            if (zp) zw_next = __ldg(zrow + (k >> (lg + 3)));
-        }
-        int g_cur = -1;
-        uint32_t s2 = 0, zmagic = 0x64006400u, zneg16 = 0;
-        const uint32_t wline = smem_u32(smem + C::kWOff) + (uint32_t)(h * (C::kWBytes / 2) + r * 128);
+        // scales and zeros of the stage's groups (256 / G, all in one zero word) are fetched a stage ahead;
+        // with whole stages the scales are one aligned load
+        constexpr int kGPS = 64 * kTcWKB / G;
+        const bool whole = a.K % (64 * kTcWKB) == 0;
+        uint32_t sc[(kGPS + 1) / 2] = {}, zw = 0x88888888u, sc_next[(kGPS + 1) / 2] = {}, zw_next = 0x88888888u;
+        auto fetch = [&](int g0) {
+            if (g0 >= ng) return;
+            if (whole) {
+                if constexpr (kGPS == 8) {
+                    const uint4 t = __ldg(reinterpret_cast<const uint4*>(srow + g0));
+                    sc_next[0] = t.x, sc_next[1] = t.y, sc_next[2] = t.z, sc_next[3] = t.w;
+                } else if constexpr (kGPS == 4) {
+                    const uint2 t = __ldg(reinterpret_cast<const uint2*>(srow + g0));
+                    sc_next[0] = t.x, sc_next[1] = t.y;
+                } else if constexpr (kGPS == 2) {
+                    sc_next[0] = __ldg(reinterpret_cast<const uint32_t*>(srow + g0));
+                } else {
+                    sc_next[0] = __ldg(srow + g0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < (kGPS + 1) / 2; ++i) {
+                    sc_next[i] = g0 + 2 * i < ng ? __ldg(srow + g0 + 2 * i) : 0u;
+                    if (kGPS > 1 && g0 + 2 * i + 1 < ng) sc_next[i] |= (uint32_t)__ldg(srow + g0 + 2 * i + 1) << 16;
+                }
+            }
+            if (zp) zw_next = __ldg(zrow + (g0 >> 3));
+        };
+        int g0 = num_kb > 0 ? kb0 * kGemmKB / G : ng;
+        fetch(g0);
+        uint32_t s2 = 0, zmagic = 0x64006400u, zneg16 = 0, s_max = 0;
+        // row r's line of a stage; its 16-byte unit u sits at u ^ (r % 8)
+        const uint32_t wline = smem_u32(smem + C::kWOff) + (uint32_t)(h * (C::kWBytes / 2) + r * 128 + (r & 7) * 16);
+        const uint32_t part_x = (uint32_t)(part0 * 16);
         const uint32_t aline = abase + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 32 + part0 * 16);
-        int ws = 0, b = 0;
-        uint32_t wph = 0, aph = 0;
+        const uint32_t af = smem_u32(afull), ae = smem_u32(aempty);
+        int ws = 0;
+        uint32_t wph = 0, aph = 1;
 #pragma unroll 1
         for (int kb = 0; kb < num_kb; kb += kTcWKB) {
             mbar_wait_or_abort(&wfull[ws], wph, &misc[5]);
-            const int last = min(kTcWKB, num_kb - kb);
-#pragma unroll 1
-            for (int sb = 0; sb < last; ++sb) {
+            const uint32_t wr = (wline + ws * C::kWBytes) ^ part_x;
+#pragma unroll
+            for (int i = 0; i < (kGPS + 1) / 2; ++i) sc[i] = sc_next[i];
+            zw = zw_next >> (4 * (g0 & 7));
+            g0 += kGPS;
+            fetch(g0);
+            const int last = num_kb - kb;
+#pragma unroll
+            for (int sb = 0; sb < kTcWKB; ++sb) {
+                if (sb >= last) break;
+                constexpr int kBufMask = C::kABufs - 1;
+                const int b = sb & kBufMask;
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) {
-                    // (128-byte swizzle: 16-byte unit u of row r sits at u ^ (r % 8))
-                    const uint4 packed =
-                        lds128(wline + ws * C::kWBytes + (uint32_t)(((sb * 2 + part0 + i) ^ (r & 7)) << 4));
-                    const int g = k >> lg;
-                    if (g != g_cur && k < a.K) {       // (codes past K are zeros times X's zeros)
-                        g_cur = g;
-                        const uint32_t z = zp ? (zw_next >> (4 * (g & 7))) & 15u : 8u;
-                        s2 = sc_next * 0x00010001u;
+                    const uint4 packed = lds128(wr ^ (uint32_t)(sb * 32 + i * 16));
+                    // (G >= 64: both 32-code parts of a k-block are in one group; G = 32: one each)
+                    const bool fresh = G == 32 || (i == 0 && (sb * 64) % G == 0);
+                    if (fresh) {
+                        uint32_t sg, z;
+                        if constexpr (G == 32 && kParts == 1) {
+                            sg = part0 ? sc[sb] >> 16 : sc[sb] & 0xFFFFu;
+                            z = (zw >> (8 * sb + 4 * part0)) & 15u;
+                        } else {
+                            const int gi = (sb * 64 + i * 32) / G;
+                            sg = gi & 1 ? sc[gi >> 1] >> 16 : sc[gi >> 1] & 0xFFFFu;
+                            z = (zw >> (4 * gi)) & 15u;
+                        }
+                        s2 = sg * 0x00010001u;
                         zmagic = 0x64006400u + z * 0x00010001u;              // 1024 + z
                         zneg16 = 0xD400D400u + z * 0x00100010u;              // -(64 + z)
-                        // 15 scale16 may pass fp16 from 0x6C44 (4368) on: look closer there
-                        if (sc_next >= 0x6C44u && row_ok) {
-                            const float qz_max = zp ? fmaxf((float)z, 15.0f - (float)z) : 8.0f;
-                            const float sf = h2f((uint16_t)sc_next);
-                            if (!(fabsf(sf) * qz_max < 65520.0f) && !isnan(sf)) raise_error(kErrRange);
-                        }
-                        const int gn = g + gstep;
-                        if (gn < ng) {
-                            sc_next = __ldg(srow + gn);
-                            if (zp) zw_next = __ldg(zrow + (gn >> 3));
-                        }
+                        s_max = max(s_max, sg);
                     }
-                    k += kParts == 1 ? kGemmKB : 32;
                     uint32_t v[16];
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
@@ -439,7 +466,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                     }
                     // the codes are converted before the wait for the MMAs that read this buffer
                     if (i == 0) {
-                        mbar_wait_or_abort(&aempty[b], aph ^ 1u, &misc[5]);
+                        // use number (kb + sb) / kABufs of the buffer
+                        const uint32_t parity = C::kABufs == kTcWKB ? aph : (uint32_t)(((sb / C::kABufs) & 1) ^ 1);
+                        const uint32_t bar = ae + b * 8;
+                        if (!mbar_try_wait(bar, parity)) mbar_wait_or_abort(&aempty[b], parity, &misc[5]);
                         __syncwarp();
                         tc_fence_after();
                     }
@@ -448,11 +478,21 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&afull[b]);
-                if (++b == C::kABufs) b = 0, aph ^= 1u;
+                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(af + b * 8) : "memory");
             }
+            aph ^= 1u;
             if (lane == 0) mbar_arrive(&wempty[ws]);
             if (++ws == C::kWStages) ws = 0, wph ^= 1u;
+        }
+        // 15 scale16 may pass fp16 from 0x6C44 (4368) on (a negative scale or NaN counts as large here):
+        // then every group of the row is looked at
+        if (s_max >= 0x6C44u && row_ok) {
+            const int g1 = min(ng, ceil_div((kb0 + num_kb) * kGemmKB, G));
+            for (int g = kb0 * kGemmKB / G; g < g1; ++g) {
+                const uint32_t z = zp ? (__ldg(zrow + (g >> 3)) >> (4 * (g & 7))) & 15u : 8u;
+                const float sf = fabsf(h2f(__ldg(srow + g)));
+                if (!(sf * (zp ? fmaxf((float)z, 15.0f - (float)z) : 8.0f) < 65520.0f) && !isnan(sf)) raise_error(kErrRange);
+            }
         }
         const bool ok = __all_sync(0xffffffffu, num_kb > 0 && mbar_wait(tfull, 0) && misc[5] == 0);
         tc_fence_after();
@@ -624,8 +664,8 @@ inline bool make_tmap_ld(CUtensorMap* map, const void* base, CUtensorMapDataType
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
-awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
+template <int BN, int G>
+awq_status launch_tc(const LinearArgs& l, int splits, cudaStream_t st) {
     using C = TcCfg<BN>;
     CUtensorMap tx, tq;
     if (!make_tmap_ld(&tx, l.X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)l.T, (uint64_t)l.K, (uint64_t)l.ldx * 2,
@@ -634,9 +674,9 @@ awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
     if (!make_tmap_ld(&tq, l.qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, (uint64_t)l.E * l.N, (uint64_t)(l.K / 8),
                       (uint64_t)l.K / 2, 128, kTcWKB * kGemmKB / 8))
         return AWQ_ERR_CUDA;
-    const void* fn = (const void*)linear_tc_kernel<BN>;
+    const void* fn = (const void*)linear_tc_kernel<BN, G>;
     if (!prepare_kernel(fn)) return AWQ_ERR_CUDA;
-    TcArgs a = {l.X, l.ldx, l.scales, l.qzeros, l.rows, l.offsets, l.T, l.R, l.E, l.N, l.K, l.G, 0, 0, 0, l.ep};
+    TcArgs a = {l.X, l.ldx, l.scales, l.qzeros, l.rows, l.offsets, l.T, l.R, l.E, l.N, l.K, 0, 0, 0, l.ep};
     a.n_tiles = l.ep.gated ? ceil_div(l.N / 2, 128) : ceil_div(l.N, kTcRows);
     a.m_tiles = ceil_div(l.R, BN);
     const int num_kb = ceil_div(l.K, kGemmKB);
@@ -661,6 +701,16 @@ awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
     lc.numAttrs = 2;
     void* args[] = {&tx, &tq, &a};
     return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+template <int BN>
+awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
+    switch (l.G) {
+        case 32: return launch_tc<BN, 32>(l, splits, st);
+        case 64: return launch_tc<BN, 64>(l, splits, st);
+        case 128: return launch_tc<BN, 128>(l, splits, st);
+        default: return launch_tc<BN, 256>(l, splits, st);
+    }
 }
 
 // K splits (CTAs of a cluster) for `tiles` tiles on `slots` CTA slots: doubled while the tiles leave
