@@ -111,7 +111,7 @@ struct TcCfg {
     static constexpr int kRing = kXOff + kXStages * kXBytes;
     static constexpr int kSrcOff = kRing;                                  // [BN] row numbers of X (negative: none)
     static constexpr int kBarOff = kSrcOff + BN * 4;
-    static constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 2 * kABufs + 1;
+    static constexpr int kNumBars = 2 * kXStages + 2 * kWStages + 4 * kABufs + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;                // TMEM address, tile, flags
     static constexpr int kSmemBytes = kMiscOff + 32 + 1024;
     static_assert(kSmemBytes <= (kCtas == 1 ? 232448 : 115712), "shared memory");
@@ -194,9 +194,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     uint64_t* xempty = xfull + C::kXStages;         // [kXStages] MMAs done with the slot
     uint64_t* wfull = xempty + C::kXStages;         // [kWStages] packed stage landed
     uint64_t* wempty = wfull + C::kWStages;         // [kWStages] dequantisers have read it
-    uint64_t* afull = wempty + C::kWStages;         // [kABufs]   dequantised k-block in TMEM
-    uint64_t* aempty = afull + C::kABufs;           // [kABufs]   MMAs done with it
-    uint64_t* tfull = aempty + C::kABufs;           // accumulators complete
+    uint64_t* afull = wempty + C::kWStages;         // [kABufs][2] dequantised k-block of a row tile in TMEM
+    uint64_t* aempty = afull + 2 * C::kABufs;       // [kABufs][2] MMAs done with it
+    uint64_t* tfull = aempty + 2 * C::kABufs;       // accumulators complete
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     int32_t* src = reinterpret_cast<int32_t*>(smem + C::kSrcOff);
 
@@ -216,8 +216,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             mbar_init(&wfull[s], 1);
             mbar_init(&wempty[s], C::kDqWarps);
         }
-        for (int b = 0; b < C::kABufs; ++b) {
-            mbar_init(&afull[b], C::kDqWarps);
+        for (int b = 0; b < 2 * C::kABufs; ++b) {
+            mbar_init(&afull[b], C::kDqWarps / 2);
             mbar_init(&aempty[b], 1);
         }
         mbar_init(tfull, 1);
@@ -350,16 +350,21 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             int s = 0, b = 0;
             uint32_t xph = 0, aph = 0;
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait(&xfull[s], xph) || !mbar_wait(&afull[b], aph)) break;
-                tc_fence_after();
+                if (!mbar_wait(&xfull[s], xph)) break;
                 const uint64_t bdesc = bdesc0 + (uint64_t)(s * (C::kXBytes >> 4));
+                bool ok = true;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && mbar_wait(&afull[2 * b + h], aph);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kGemmKB / 16; ++kk)
                         mma_f16_ts(acc0 + h * BN, abase + (b * 2 + h) * 32 + kk * 8, bdesc + 2 * kk, idesc,
                                    (kb | kk) != 0);
-                mma_commit(&aempty[b]);
+                    mma_commit(&aempty[2 * b + h]);
+                }
+                if (!ok) break;
                 mma_commit(&xempty[s]);
                 if (++s == C::kXStages) s = 0, xph ^= 1u;
                 if (++b == C::kABufs) b = 0, aph ^= 1u;
@@ -419,7 +424,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         const uint32_t wline = smem_u32(smem + C::kWOff) + (uint32_t)(h * (C::kWBytes / 2) + r * 128 + (r & 7) * 16);
         const uint32_t part_x = (uint32_t)(part0 * 16);
         const uint32_t aline = abase + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 32 + part0 * 16);
-        const uint32_t af = smem_u32(afull), ae = smem_u32(aempty);
+        const uint32_t af = smem_u32(afull + h), ae = smem_u32(aempty + h);
         int ws = 0;
         uint32_t wph = 0, aph = 1;
 #pragma unroll 1
@@ -468,8 +473,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                     if (i == 0) {
                         // use number (kb + sb) / kABufs of the buffer
                         const uint32_t parity = C::kABufs == kTcWKB ? aph : (uint32_t)(((sb / C::kABufs) & 1) ^ 1);
-                        const uint32_t bar = ae + b * 8;
-                        if (!mbar_try_wait(bar, parity)) mbar_wait_or_abort(&aempty[b], parity, &misc[5]);
+                        if (!mbar_try_wait(ae + b * 16, parity))
+                            mbar_wait_or_abort(&aempty[2 * b + h], parity, &misc[5]);
                         __syncwarp();
                         tc_fence_after();
                     }
@@ -478,7 +483,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(af + b * 8) : "memory");
+                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(af + b * 16) : "memory");
             }
             aph ^= 1u;
             if (lane == 0) mbar_arrive(&wempty[ws]);
