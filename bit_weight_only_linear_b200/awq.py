@@ -345,18 +345,17 @@ def _refuse(t, name, index, shape, dtypes, what):
     raise ValueError(f"{name} must {what}")
 
 
-def _rows(t: Optional[torch.Tensor], name: str, index: int, shape, dtypes=_F16):
-    """(data pointer, distance of rows in elements) of a 2-D tensor with contiguous rows."""
+def _rows(t: Optional[torch.Tensor], name: str, index: int, rows: int, cols: int, dtype=torch.float16):
+    """(data pointer, distance of rows in elements) of a [rows][cols] tensor with contiguous rows."""
     if t is None:
         return 0, 0
-    if t.get_device() != index or t.dtype not in dtypes or t.shape != shape:
-        _refuse(t, name, index, shape, dtypes, "")
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (rows, cols):
+        _refuse(t, name, index, (rows, cols), (dtype,), "")
     ld, inner = t.stride()
-    cols = shape[1]
-    if shape[0] <= 1:
+    if rows <= 1:
         ld = (cols + 7) // 8 * 8       # one row or none: any distance does
     if ld < cols or (inner != 1 and cols > 1):
-        _refuse(t, name, index, shape, dtypes, "have contiguous rows that do not overlap")
+        _refuse(t, name, index, (rows, cols), (dtype,), "have contiguous rows that do not overlap")
     return t.data_ptr(), ld
 
 
@@ -364,22 +363,29 @@ def _flat(t: Optional[torch.Tensor], name: str, index: int, shape, dtypes) -> in
     """Data pointer of a contiguous tensor of the given shape."""
     if t is None:
         return 0
-    if t.get_device() != index or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+    if t.dtype not in dtypes or t.get_device() != index or t.shape != shape or not t.is_contiguous():
         _refuse(t, name, index, shape, dtypes, "be contiguous")
     return t.data_ptr()
 
 
-def _on(index: int, fn_name: str, stream, *args) -> None:
-    """Call the entry point with device `index` current, on `stream` or the device's current stream."""
-    fn = getattr(_lib or load_library(), fn_name)
-    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-    if torch._C._cuda_getDevice() == index:
-        status = fn(*args, st)
-    else:
-        with torch.cuda.device(index):
+def _entry(fn_name: str):
+    """The entry point as f(index, stream, *args): called with device `index` current, on `stream` or the
+    device's current stream."""
+    def call(index, stream, *args):
+        fn = getattr(_lib or load_library(), fn_name)
+        st = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+        if torch._C._cuda_getDevice() == index:
             status = fn(*args, st)
-    if status != AWQ_OK:
-        raise AWQError(fn_name, status)
+        else:
+            with torch.cuda.device(index):
+                status = fn(*args, st)
+        if status:
+            raise AWQError(fn_name, status)
+    return call
+
+
+_linear_fused, _linear_grouped, _moe_route, _moe_combine = map(
+    _entry, ("awq_linear_fused", "awq_linear_grouped", "awq_moe_route", "awq_moe_combine"))
 
 
 def _cuda(t: torch.Tensor, name: str, dims: int = 2):
@@ -427,10 +433,10 @@ def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bi
     n_out = N // 2 if gated else N
     if out is None:
         out = X.new_empty((M, n_out))
-    px, ldx = _rows(X, "X", dev, (M, K))
-    pr, ldr = _rows(residual, "residual", dev, (M, n_out))
-    py, ldy = _rows(out, "out", dev, (M, n_out))
-    _on(dev, "awq_linear_fused", stream, px, M, ldx, pq, ps, pz, N, K, _config(group_size, zero_point),
+    px, ldx = _rows(X, "X", dev, M, K)
+    pr, ldr = _rows(residual, "residual", dev, M, n_out)
+    py, ldy = _rows(out, "out", dev, M, n_out)
+    _linear_fused(dev, stream, px, M, ldx, pq, ps, pz, N, K, _config(group_size, zero_point),
         _flat(bias, "bias", dev, (N,), _F16), act, 1 if gated else 0, pr, ldr, py, ldy)
     return out
 
@@ -457,9 +463,9 @@ def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=12
     R = T if rows is None else rows.shape[0]
     if out is None:
         out = X.new_empty((R, n_out))
-    px, ldx = _rows(X, "X", dev, (T, K))
-    py, ldy = _rows(out, "out", dev, (R, n_out))
-    _on(dev, "awq_linear_grouped", stream, px, T, ldx, _flat(rows, "rows", dev, (R,), _I32), R,
+    px, ldx = _rows(X, "X", dev, T, K)
+    py, ldy = _rows(out, "out", dev, R, n_out)
+    _linear_grouped(dev, stream, px, T, ldx, _flat(rows, "rows", dev, (R,), _I32), R,
         _flat(offsets, "offsets", dev, (E + 1,), _I32), E, pq, ps, pz, N, K, _config(group_size, zero_point),
         _flat(bias, "bias", dev, (E, N), _F16), act, 1 if gated else 0, py, ldy)
     return out
@@ -486,7 +492,7 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
     score = SCORINGS.get(scoring)
     if score is None:
         raise ValueError(f"scoring {scoring!r} is not one of {sorted(SCORINGS)}")
-    pl, ld = _rows(logits, "logits", dev, (T, E), _LOGITS)
+    pl, ld = _rows(logits, "logits", dev, T, E, torch.float16 if half else torch.float32)
     if out is None:
         experts, positions, rows = logits.new_empty((3, T, top_k), dtype=torch.int32).unbind()
         out = MoeRoute(logits.new_empty((T, top_k), dtype=torch.float32), experts,
@@ -501,14 +507,14 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
                 workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                         else torch.cuda.ExternalStream(_stream(stream), device=logits.device))
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _on(dev, "awq_moe_route", stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0,
+    _moe_route(dev, stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0,
         _flat(weights, "weights", dev, slots, _F32), _flat(experts, "experts", dev, slots, _I32),
         _flat(offsets, "offsets", dev, (E + 1,), _I32), _flat(rows, "rows", dev, (T * top_k,), _I32),
         _flat(positions, "positions", dev, slots, _I32), ws, ws_bytes)
     return out
 
 
-_F32, _LOGITS = (torch.float32,), (torch.float32, torch.float16)
+_F32 = (torch.float32,)
 _ROUTE_SINGLE = 256      # tokens up to which routing is one block and needs no workspace
 
 
@@ -533,9 +539,9 @@ def moe_combine(Y, weights, positions, residual=None, out=None, stream=None) -> 
     T, k = slots = positions.shape
     if out is None:
         out = Y.new_empty((T, N))
-    py, ldy = _rows(Y, "Y", dev, (R, N))
-    pr, ldr = _rows(residual, "residual", dev, (T, N))
-    po, ldo = _rows(out, "out", dev, (T, N))
-    _on(dev, "awq_moe_combine", stream, py, R, ldy, _flat(weights, "weights", dev, slots, _F32),
+    py, ldy = _rows(Y, "Y", dev, R, N)
+    pr, ldr = _rows(residual, "residual", dev, T, N)
+    po, ldo = _rows(out, "out", dev, T, N)
+    _moe_combine(dev, stream, py, R, ldy, _flat(weights, "weights", dev, slots, _F32),
         _flat(positions, "positions", dev, slots, _I32), T, k, N, pr, ldr, po, ldo)
     return out

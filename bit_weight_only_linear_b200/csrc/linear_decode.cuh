@@ -496,10 +496,10 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
 // ---------------------------------------------------------------------------
 
 // Rows of X at a time and stages that fit in `smem` bytes: as many rows as there are, up to 8, with
-// at least three stages.  false if not even one row fits.
+// at least two stages.  false if not even one row fits.
 inline bool dec_plan(int rows, int K, int G, int smem, int& mc, int& S) {
     for (mc = std::min(rows, kDecMaxRows); mc >= 1; --mc)
-        for (S = 6; S >= 3; --S)
+        for (S = 6; S >= 2; --S)
             if (DecSmem(mc, K, G, S).bytes() <= smem) return true;
     return false;
 }
@@ -533,12 +533,15 @@ inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d,
     return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
 }
 
-// Which form takes a call.  The decode form reads the weights once per 8 rows of a matrix and needs
-// whole 128-code blocks; above that the tensor-core tiles win.
+// Which form takes a call.  The decode form takes up to 8 rows a matrix and whole 128-code blocks; above
+// that the tensor-core tiles win.  Where X's rows do not all fit in shared memory it needs a second pass
+// over the weights, which pays while that comes from L2 (8 rows x 14336, 4096 channels: 20 us against 22 for
+// the tiles; 3 rows x 28672, 8192 channels, 117 MB: 61 us against 48).
 inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaStream_t st) {
     const int share = l.offsets ? ceil_div(l.R, std::min(l.R, l.E)) : l.R;
     int mc = 0, S = 0;
-    if (share <= kDecMaxRows && l.K % 128 == 0 && dec_plan(l.R, l.K, l.G, d.max_smem_optin, mc, S) && mc >= share) {
+    if (share <= kDecMaxRows && l.K % 128 == 0 && dec_plan(l.R, l.K, l.G, d.max_smem_optin, mc, S) &&
+        (mc >= share || (!l.offsets && 2 * mc >= share && (long long)l.N * l.K <= (128LL << 20)))) {
         // a CTA's list of segments must hold the row sets that its units may reach
         const long long sets = l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc);
         if (sets <= (long long)(kDecMaxSegs - 2) * d.sms && sets * ceil_div(l.N, 32) < 0x7fffffffLL)

@@ -26,6 +26,10 @@
 // what it issued, frees TMEM and returns.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
 #include "common.cuh"
 #include "epilogue.cuh"
 #include "gemm_sm100.cuh"
@@ -61,11 +65,11 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrive on `bar` once every cp.async of this thread so far has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -105,6 +109,7 @@ struct TcCfg {
     static constexpr int kXStages = BN == 192 ? 5 : (BN == 128 ? 6 : (BN == 64 ? 5 : (BN == 32 ? 10 : 6)));
     static constexpr int kWStages = BN == 64 || BN == 32 ? 2 : 3;
     static constexpr int kXBytes = BN * 128;
+    static constexpr int kXBox = BN < 32 ? 16 : 32;                        // rows per copy of X
     static constexpr int kWBytes = kTcRows * 32 * kTcWKB;
     static constexpr int kWOff = 0;
     static constexpr int kXOff = kWOff + kWStages * kWBytes;
@@ -249,7 +254,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         }
         if (t.x >= 0 && a.rows)
             for (int c = lane; c < BN; c += 32) {
-                const int s = t.y + c < t.z ? __ldg(a.rows + t.y + c) : -1;
+                // (columns behind the tile's rows are never stored: any row does)
+                const int s = __ldg(a.rows + min(t.y + c, t.z - 1));
                 src[c] = s < a.T ? s : -1;
             }
         if (lane == 0) misc[5] = 0u;
@@ -266,56 +272,68 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     const int end0 = F, end1 = a.N;
     const int kb0 = rank * a.kb_per;
     const int num_kb = expert < 0 ? 0 : max(0, min(a.kb_per, ceil_div(a.K, kGemmKB) - kb0));
+    const int n16 = (r1 - r0 + 15) & ~15;             // columns of the MMA: the tile's rows of X
+    const int boxes = (n16 + C::kXBox - 1) / C::kXBox;
     const uint32_t acc0 = tmem, abase = tmem + 2 * BN;
 
     if (warp < C::kXWarps) {
         // ---------------- X ring ----------------
         if (a.rows) {
-            // thread: 16-byte unit u of rows t0, t0 + kXWarps * 4, ..; zeros for rows that do not exist
-            // and past K.  A stage is handed over once the copies of the kAhead stages behind it are
-            // under way: its own have landed then.
-            constexpr int kRowStep = C::kXWarps * 4, kRows = BN / kRowStep, kAhead = C::kXStages - 2;
+            // thread: 16-byte unit u of rows t0, t0 + kRowStep, ..; its arrival on the stage's barrier follows
+            // when its copies have landed.  They are generic writes: the MMA's thread fences them (a fence
+            // here would wait for the copies still under way).
+            constexpr int kRowStep = C::kXWarps * 4, kRows = BN / kRowStep;
             const int u = threadIdx.x & 7, t0 = threadIdx.x >> 3;
-            uint32_t off[kRows];                    // row starts in 16-byte units; all ones: no row
+            const int count = num_kb > 0 ? n16 / kRowStep : 0;          // rows of this thread
+            uint32_t off[kRows];                                        // row starts in 16-byte units
+            bool all = true;                                            // every row lies inside X
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                const int r = num_kb > 0 ? src[t0 + i * kRowStep] : -1;
+                const int r = i < count ? src[t0 + i * kRowStep] : 0;
+                all = all && r >= 0;
                 off[i] = r < 0 ? 0xffffffffu : (uint32_t)((unsigned long long)r * (unsigned long long)(a.ldx >> 3));
             }
+            all = __all_sync(0xffffffffu, all);
             const uint32_t dst0 = smem_u32(smem + C::kXOff) + (uint32_t)(t0 * 128 + ((u ^ (t0 & 7)) << 4));
-            int s = 0, d = 0;
+            int s = 0;
             uint32_t ph = 0;
-            for (int j = 0; j < num_kb + kAhead; ++j) {
-                if (j < num_kb) {
-                    mbar_wait_or_abort(&xempty[s], ph ^ 1u, &misc[5]);
-                    const int unit = (kb0 + j) * (kGemmKB / 8) + u;
-                    const bool in_k = unit * 8 < a.K;
+            for (int j = 0; j < num_kb; ++j) {
+                mbar_wait_or_abort(&xempty[s], ph ^ 1u, &misc[5]);
+                const int unit = (kb0 + j) * (kGemmKB / 8) + u;
+                const uint4* base = reinterpret_cast<const uint4*>(a.X) + unit;
+                const uint32_t dst = dst0 + (uint32_t)(s * C::kXBytes);
+                const bool in_k = unit * 8 < a.K;
+                if (all && __all_sync(0xffffffffu, in_k)) {
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) {
-                        // (rows 4 or 8 apart: the swizzle follows row % 8)
+                        // (rows 4 apart: the swizzle follows row % 8)
                         const uint32_t flip = kRowStep % 8 ? (uint32_t)((i & 1) * 64) : 0u;
-                        const bool live = in_k && off[i] != 0xffffffffu;
-                        cp_async16((dst0 ^ flip) + (uint32_t)(s * C::kXBytes + i * kRowStep * 128),
-                                   a.X + (live ? ((size_t)off[i] + unit) * 8 : 0), live);
+                        if (i < count) cp_async16((dst ^ flip) + (uint32_t)(i * kRowStep * 128), base + off[i], true);
                     }
-                    if (++s == C::kXStages) s = 0, ph ^= 1u;
+                } else {
+                    // zeros past K and for rows that do not exist
+#pragma unroll 1
+                    for (int i = 0; i < count; ++i) {
+                        const uint32_t flip = kRowStep % 8 ? (uint32_t)((i & 1) * 64) : 0u;
+                        const int r = src[t0 + i * kRowStep];
+                        const bool live = in_k && r >= 0;
+                        cp_async16((dst ^ flip) + (uint32_t)(i * kRowStep * 128),
+                                   live ? a.X + r * a.ldx + unit * 8 : a.X, live);
+                    }
                 }
-                cp_async_commit();
-                if (j >= kAhead) {
-                    cp_async_wait<kAhead>();
-                    fence_proxy_async_smem();       // generic writes -> visible to the MMA
-                    mbar_arrive(&xfull[d]);
-                    if (++d == C::kXStages) d = 0;
-                }
+                cp_async_arrive(&xfull[s]);
+                if (++s == C::kXStages) s = 0, ph ^= 1u;
             }
-            cp_async_wait<0>();
+            cp_async_wait_all();        // before the CTA exits, or its ring is reused
         } else if (warp == 0 && elect_one()) {
             int issued = 0, s = 0;
             uint32_t ph = 0;
             for (int j = 0; j < num_kb; ++j) {
                 if (!mbar_wait(&xempty[s], ph ^ 1u)) break;
-                mbar_arrive_expect_tx(&xfull[s], C::kXBytes);
-                tma_load_2d(smem + C::kXOff + s * C::kXBytes, &tmap_x, &xfull[s], (kb0 + j) * kGemmKB, r0);
+                mbar_arrive_expect_tx(&xfull[s], (uint32_t)(boxes * C::kXBox * 128));
+                for (int i = 0; i < boxes; ++i)
+                    tma_load_2d(smem + C::kXOff + s * C::kXBytes + i * C::kXBox * 128, &tmap_x, &xfull[s],
+                                (kb0 + j) * kGemmKB, r0 + i * C::kXBox);
                 ++issued;
                 if (++s == C::kXStages) s = 0, ph ^= 1u;
             }
@@ -345,12 +363,13 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     } else if (warp == C::kMmaWarp) {
         if (elect_one()) {
             // ---------------- MMA issuer ----------------
-            const uint32_t idesc = idesc_f16_f32(128, (r1 - r0 + 15) & ~15);    // as many columns as there are rows
+            const uint32_t idesc = idesc_f16_f32(128, n16);
             const uint64_t bdesc0 = desc_sw128_kmajor(smem_u32(smem + C::kXOff));
             int s = 0, b = 0;
             uint32_t xph = 0, aph = 0;
             for (int kb = 0; kb < num_kb; ++kb) {
                 if (!mbar_wait(&xfull[s], xph)) break;
+                if (a.rows) fence_proxy_async_smem();
                 const uint64_t bdesc = bdesc0 + (uint64_t)(s * (C::kXBytes >> 4));
                 bool ok = true;
 #pragma unroll
@@ -674,7 +693,7 @@ awq_status launch_tc(const LinearArgs& l, int splits, cudaStream_t st) {
     using C = TcCfg<BN>;
     CUtensorMap tx, tq;
     if (!make_tmap_ld(&tx, l.X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)l.T, (uint64_t)l.K, (uint64_t)l.ldx * 2,
-                      BN, kGemmKB))
+                      C::kXBox, kGemmKB))
         return AWQ_ERR_CUDA;
     if (!make_tmap_ld(&tq, l.qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, (uint64_t)l.E * l.N, (uint64_t)(l.K / 8),
                       (uint64_t)l.K / 2, 128, kTcWKB * kGemmKB / 8))
@@ -718,29 +737,81 @@ awq_status launch_tc_bn(const LinearArgs& l, int splits, cudaStream_t st) {
     }
 }
 
-// K splits (CTAs of a cluster) for `tiles` tiles on `slots` CTA slots: doubled while the tiles leave
-// at least half of the slots idle and a split keeps two packed stages (512 codes).
-inline int tc_splits(long long tiles, int slots, int K) {
-    int s = 1;
-    while (s < kTcMaxSplits && tiles * s * 2 <= slots && ceil_div(K, kGemmKB * kTcWKB) >= 4 * s) s *= 2;
-    return s;
+// Clusters of `splits` CTAs that can be resident at once on the current device, per kernel (a driver
+// query, made once: the GPU's processing clusters do not divide evenly; of 8 CTAs with one on each SM, a
+// B200 holds 15 clusters, of 6 CTAs 22, of 4 CTAs 33).
+template <int BN>
+int tc_active_clusters(int splits) {
+    using C = TcCfg<BN>;
+    static std::mutex mu;
+    static int known[64][kTcMaxSplits + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    int& n = known[dev][splits];
+    if (n == 0) {
+        const void* fn = (const void*)linear_tc_kernel<BN, 128>;
+        if (!prepare_kernel(fn)) return 0;
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3((unsigned)splits);
+        lc.blockDim = dim3(C::kThreads);
+        lc.dynamicSmemBytes = C::kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)splits;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &lc) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = -1;
+        }
+    }
+    return n;
+}
+
+// Modelled time (us) of `tiles` tiles of `rows` rows of X with the K in `splits` parts, from measured
+// slopes: a k-block of 256 weight rows takes 0.30 us, or 3.5 ns per row of X (0.38 and 3.0 in the 192-row form); a
+// tile 4 us (6) around them, and 7 (12) for the exchange of a split's partial sums.  A last partial wave
+// costs half of one on average.
+template <int BN>
+double tc_time(long long tiles, int rows, int num_kb, int splits) {
+    const int active = tc_active_clusters<BN>(splits);
+    if (active < 1) return 1e30;
+    const int kb = ceil_div(ceil_div(num_kb, splits), kTcWKB) * kTcWKB;
+    double waves = (double)tiles / active;
+    waves = waves <= 1.0 ? 1.0 : std::min(std::ceil(waves), waves + 0.5);
+    double t = kb * (BN == 192 ? std::max(0.38, 0.0030 * rows) : std::max(0.30, 0.0035 * rows)) + (BN == 192 ? 6.0 : 4.0);
+    if (splits > 1) t += BN == 192 ? 12.0 : 7.0;
+    return waves * t;
 }
 
 inline awq_status launch_linear_tc(const LinearArgs& l, int sms, cudaStream_t st) {
-    // rows per tile: the dense batch, or the experts' average share of the rows
+    // rows to plan for: the dense batch, or the experts' average share with a margin for uneven ones
     const int active = l.offsets ? std::min(l.R, l.E) : 1;
-    const int share = ceil_div(l.R, active);
-    const int bn = share <= 16 ? 16 : share <= 32 ? 32 : share <= 64 ? 64 : share <= 128 ? 128 : 192;
+    const int m = l.offsets ? (int)std::min<long long>(l.R, ((long long)l.R * 13 + active * 10 - 1) / (active * 10)) : l.R;
     const int n_tiles = l.ep.gated ? ceil_div(l.N / 2, 128) : ceil_div(l.N, kTcRows);
-    const long long tiles = (long long)active * ceil_div(share, bn) * n_tiles;
-    const int splits = tc_splits(tiles, sms * (bn <= 64 ? 2 : 1), l.K);
-    switch (bn) {
-        case 16: return launch_tc_bn<16>(l, splits, st);
-        case 32: return launch_tc_bn<32>(l, splits, st);
-        case 64: return launch_tc_bn<64>(l, splits, st);
-        case 128: return launch_tc_bn<128>(l, splits, st);
-        default: return launch_tc_bn<192>(l, splits, st);
+    const int num_kb = ceil_div(l.K, kGemmKB);
+    // Few rows and many tiles: two CTAs on an SM hide each other's start and end (64 experts of 9 rows, 2816 x
+    // 2048: 72 us at 16 rows a tile against 101 with one CTA; with fewer tiles than SMs it is the reverse,
+    // 16 tiles of 61 rows x 14336 in 6 parts: 25 us against 28)
+    if (m <= 64 && 2LL * active * n_tiles >= 3LL * sms) {
+        if (m <= 16) return launch_tc_bn<16>(l, 1, st);
+        if (m <= 32) return launch_tc_bn<32>(l, 1, st);
+        return launch_tc_bn<64>(l, 1, st);
     }
+    int best = 1;
+    bool wide = false;
+    double best_t = 1e30;
+    for (int w = 0; w < 2; ++w) {
+        const int mt = ceil_div(m, w ? 192 : 128), rows = (ceil_div(m, mt) + 15) & ~15;
+        const long long tiles = (long long)active * mt * n_tiles;
+        for (int s = 1; s <= kTcMaxSplits && (s == 1 || num_kb >= 4 * s); ++s) {
+            const double t = w ? tc_time<192>(tiles, rows, num_kb, s) : tc_time<128>(tiles, rows, num_kb, s);
+            if (t < best_t) best_t = t, best = s, wide = w;
+        }
+    }
+    return wide ? launch_tc_bn<192>(l, best, st) : launch_tc_bn<128>(l, best, st);
 }
 
 }  // namespace awq
