@@ -515,7 +515,7 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
 
 
 _F32 = (torch.float32,)
-_ROUTE_SINGLE = 256      # tokens up to which routing is one block and needs no workspace
+_ROUTE_SINGLE = 32      # tokens up to which routing is one block and needs no workspace
 
 
 def _route_need(T: int, E: int, index: int) -> int:

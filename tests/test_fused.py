@@ -286,7 +286,7 @@ def _check_route(r, logits, k, scoring, renorm):
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 7, 7), (31, 33, 4), (32, 64, 6), (33, 128, 8), (100, 5, 1),
                                    (256, 16, 2), (257, 60, 4), (1000, 200, 10), (700, 257, 32), (300, 1024, 32),
-                                   (5000, 8, 2)])
+                                   (5000, 8, 2), (13000, 40, 7), (12300, 130, 3), (12288, 9, 2)])
 @pytest.mark.parametrize("half", [False, True])
 @pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 def test_moe_route(lib, T, E, k, half, scoring, renorm):
