@@ -13,6 +13,9 @@
 //   * A persistent CTA per SM takes a contiguous range of units: all of one dense matrix, or the
 //     units of the experts that have rows (8 rows of an expert at a time), so that X is staged once
 //     per expert and CTA.
+//   * With many units per CTA a unit is 64 rows and a stage 64 rows x 1024 codes (RS = 2): 8 warps split
+//     the K of each half, so half as many partial sums meet per row.  With few, 32 rows (RS = 1) share out
+//     more evenly.
 //   * Warps: a producer (3-D TMA, 32 KB stages of 32 rows x 2048 codes), two converters (scales and
 //     zeros -> fp32 pairs per stage), 16 consumers (128 codes of a stage each), a reducer (the
 //     consumers' partial sums in a fixed order, then the epilogue).
@@ -32,24 +35,25 @@ constexpr int kDecConsumers = 16;
 constexpr int kDecConverters = 2;
 constexpr int kDecReducer = 1 + kDecConverters, kDecConsumer0 = kDecReducer + 1;   // first warps of the roles
 constexpr int kDecThreads = (kDecConsumer0 + kDecConsumers) * 32;
-constexpr int kDecRows = 32;                     // weight rows per unit
-constexpr int kDecKC = 2048;                     // codes per row and stage
-constexpr int kDecStageBytes = kDecRows * kDecKC / 2;
+constexpr int kDecRows = 32;                     // weight rows of a consumer: two MMA row tiles
+constexpr int kDecStageBytes = 32 * 1024;        // 32 RS rows x 2048 / RS codes
 constexpr int kDecMaxRows = 8;                   // rows of X at a time (MMA N)
+constexpr int kDecManyUnits = 8;                 // 32-row units per CTA from which a unit is 64 rows
 constexpr int kDecMaxSegs = 32;                  // segments of a CTA
 constexpr int kDecPartPitch = 36;                // words per row of X in a partial sum (bank spread)
 
 struct DecSmem {
-    int K, M, S, Kp, nsteps, gpc;
-    __host__ __device__ DecSmem(int M_, int K_, int G, int S_) : K(K_), M(M_), S(S_) {
-        Kp = (K + kDecKC - 1) / kDecKC * kDecKC;
+    int K, M, S, RS, Kp, nsteps, gpc;
+    __host__ __device__ DecSmem(int M_, int K_, int G, int S_, int RS_) : K(K_), M(M_), S(S_), RS(RS_) {
+        const int kc = 2048 / RS;                // codes per row and stage
+        Kp = (K + kc - 1) / kc * kc;
         nsteps = Kp / (32 * gemv_words_per_thread(G));
-        gpc = kDecKC / G;
+        gpc = kc / G;
     }
-    // converted (scale, scale * zero) pairs of a stage: [32 rows][gpc], rows padded by 16 bytes
+    // converted (scale, scale * zero) pairs of a stage: [32 RS rows][gpc], rows padded by 16 bytes
     __host__ __device__ int cvt_pitch() const { return gpc * 8 + 16; }
     __host__ __device__ int cvt() const { return S * kDecStageBytes; }
-    __host__ __device__ int x() const { return cvt() + S * kDecRows * cvt_pitch(); }
+    __host__ __device__ int x() const { return cvt() + S * kDecRows * RS * cvt_pitch(); }
     __host__ __device__ int x_pitch() const { return Kp * 2 + 64; }
     __host__ __device__ int xsum() const { return x() + M * x_pitch(); }
     __host__ __device__ int part() const { return (xsum() + M * nsteps * 4 + 15) & ~15; }
@@ -126,16 +130,19 @@ struct DecIter {
     }
 };
 
-template <int G>
+template <int G, int RS>
 __global__ void __launch_bounds__(kDecThreads, 1)
 linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a) {
     using namespace sm100;
     constexpr int WT = gemv_words_per_thread(G);
     constexpr int kStepCodes = 32 * WT;
     constexpr int Q = 128 / kStepCodes;                    // k-steps of a consumer per stage
-    constexpr int GPC = kDecKC / G;                        // groups per stage
+    constexpr int KC = 2048 / RS;                          // codes per row and stage
+    constexpr int GPC = KC / G;                            // groups per row and stage
+    constexpr int KS = kDecConsumers / RS;                 // consumers that share the K of 32 rows
+    constexpr int kSub = kDecStageBytes / RS;              // their part of a stage
     extern __shared__ __align__(128) uint8_t smem[];
-    const DecSmem L(a.mc, a.K, G, a.S);
+    const DecSmem L(a.mc, a.K, G, a.S, RS);
     const int S = a.S;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars());   // weights and converted pairs in
     uint64_t* empty = full + S;                    // consumers done with a stage
@@ -176,12 +183,12 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     }
     __syncthreads();
     const int nseg = (int)abort[1];
-    const int nchunks = L.Kp / kDecKC;
+    const int nchunks = L.Kp / KC;
     const int F = a.ep.gated ? a.N / 2 : a.N;
     const uint32_t sbase = smem_u32(smem);
-    // first rows of the two row tiles of unit n
-    auto tile0 = [&](int n) { return a.ep.gated ? n * 16 : n * kDecRows; };
-    auto tile1 = [&](int n) { return a.ep.gated ? F + n * 16 : n * kDecRows + 16; };
+    // first rows of the two row tiles of part p of unit n
+    auto tile0 = [&](int n, int p) { return (n * RS + p) * (a.ep.gated ? 16 : 32); };
+    auto tile1 = [&](int n, int p) { return a.ep.gated ? F + (n * RS + p) * 16 : (n * RS + p) * 32 + 16; };
 
     if (warp == 0) {
         // ---------------- producer ----------------
@@ -191,16 +198,19 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         for (int i = 0; i < nseg && ok; ++i) {
             const DecSeg sg = segs[i];
             for (int n = sg.n; n < sg.n + sg.count && ok; ++n) {
-                const int ra = sg.expert * a.N + tile0(n), rb = sg.expert * a.N + tile1(n);
                 for (int c = 0; c < nchunks; ++c) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u));
                     if (!ok) break;
                     if (elect_one()) {
                         uint8_t* dst = smem + (size_t)st * kDecStageBytes;
-                        // boxes {16 words, 16 rows, 16 blocks of 128 codes}; blocks past K are zeros
+                        // boxes {16 words, 16 rows, KC / 128 blocks of 128 codes}; blocks past K are zeros
                         mbar_arrive_expect_tx(&full[st], kDecStageBytes);
-                        tma_load_3d(dst, &tmap_q, &full[st], 0, ra, c * (kDecKC / 128));
-                        tma_load_3d(dst + kDecStageBytes / 2, &tmap_q, &full[st], 0, rb, c * (kDecKC / 128));
+#pragma unroll
+                        for (int p = 0; p < RS; ++p) {
+                            tma_load_3d(dst + p * kSub, &tmap_q, &full[st], 0, sg.expert * a.N + tile0(n, p), c * (KC / 128));
+                            tma_load_3d(dst + p * kSub + kSub / 2, &tmap_q, &full[st], 0, sg.expert * a.N + tile1(n, p),
+                                        c * (KC / 128));
+                        }
                     }
                     __syncwarp();
                     ++issued;
@@ -213,10 +223,11 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         return;
     }
     if (warp < kDecReducer) {
-        // ---------------- converters: lane = row of the unit.  Each takes every second stage and holds
+        // ---------------- converters: lane = row of each part of the unit.  Each takes every second stage and holds
         // the scales and zero words of the next kDepth of them in registers (a stage's loads take longer
         // than the stage streams) ----------------
-        constexpr int OCT = GPC / 8;                           // octets of groups per row and stage
+        static_assert(GPC % 8 == 0, "whole octets of groups per row and stage");
+        constexpr int OPR = GPC / 8, OCT = RS * OPR;           // octets of groups per row, per lane and stage
         constexpr int kDepth = OCT <= 4 ? 2 : 1;
         const int ng = a.K / G, nzw = ceil_div(ng, 8);
         const bool zp = a.qzeros != nullptr;
@@ -225,23 +236,28 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         uint32_t zw[kDepth][OCT];
         auto fetch = [&](const DecIter& it, uint4 (&fs)[OCT], uint32_t (&fz)[OCT]) {
             if (!it.live()) return;
-            const int row = lane < 16 ? tile0(it.n) + lane : tile1(it.n) + lane - 16;
-            const int lim = a.ep.gated && lane < 16 ? F : a.N;
-            const size_t wr = (size_t)it.sg->expert * a.N + min(row, lim - 1);   // rows past the end: dropped later
-            const uint16_t* sp = a.scales + wr * ng;
 #pragma unroll
             for (int o = 0; o < OCT; ++o) {
-                const int g0 = it.c * GPC + 8 * o;
-                fs[o] = make_uint4(0u, 0u, 0u, 0u);                             // groups past K: scale 0
+                const int p = o / OPR;
+                const int row = lane < 16 ? tile0(it.n, p) + lane : tile1(it.n, p) + lane - 16;
+                const int lim = a.ep.gated && lane < 16 ? F : a.N;
+                const size_t wr = (size_t)it.sg->expert * a.N + min(row, lim - 1);   // rows past the end: dropped later
+                const uint16_t* sp = a.scales + wr * ng;
+                const int g0 = it.c * GPC + 8 * (o % OPR);
+                fs[o] = make_uint4(0u, 0u, 0u, 0u);                                  // groups past K: scale 0
                 fz[o] = 0x88888888u;
                 if (g0 < ng) {
                     if (vec) {
                         fs[o] = __ldg(reinterpret_cast<const uint4*>(sp + g0));
                     } else {
-                        uint32_t h[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] = g0 + i < ng ? __ldg(sp + g0 + i) : 0u;
-                        fs[o] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                        unsigned long long w[2] = {0ull, 0ull};
+#pragma unroll 1
+                        for (int i = 0; i < 8 && g0 + i < ng; ++i) {
+                            const unsigned long long v = (unsigned long long)__ldg(sp + g0 + i) << (16 * (i & 3));
+                            if (i < 4) w[0] |= v;
+                            else w[1] |= v;
+                        }
+                        fs[o] = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
                     }
                     if (zp) fz[o] = __ldg(a.qzeros + wr * nzw + (g0 >> 3));
                 }
@@ -263,15 +279,16 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
             for (int d = 0; d < kDepth; ++d) {
                 if (!it.live()) break;
                 mbar_wait_or_abort(&empty[st], ph ^ 1u, abort);
-                float4* dst = reinterpret_cast<float4*>(smem + L.cvt() + (st * kDecRows + lane) * L.cvt_pitch());
+                uint8_t* rows = smem + L.cvt() + (st * RS * kDecRows + lane) * L.cvt_pitch();
 #pragma unroll
                 for (int o = 0; o < OCT; ++o) {
+                    float4* dst = reinterpret_cast<float4*>(rows + o / OPR * kDecRows * L.cvt_pitch()) + o % OPR * 4;
                     const uint32_t hw[4] = {sc[d][o].x, sc[d][o].y, sc[d][o].z, sc[d][o].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float s0 = h2f((uint16_t)(hw[k] & 0xFFFFu)), s1 = h2f((uint16_t)(hw[k] >> 16));
                         const float z0 = (float)((zw[d][o] >> (8 * k)) & 15u), z1 = (float)((zw[d][o] >> (8 * k + 4)) & 15u);
-                        dst[o * 4 + k] = make_float4(s0 * 16777216.0f, s0 * z0, s1 * 16777216.0f, s1 * z1);
+                        dst[k] = make_float4(s0 * 16777216.0f, s0 * z0, s1 * 16777216.0f, s1 * z1);
                     }
                 }
                 __syncwarp();
@@ -299,46 +316,50 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
             const DecSeg sg = segs[i];
             const uint16_t* bias = ep.bias ? ep.bias + (size_t)sg.expert * a.N : nullptr;
             for (int n = sg.n; n < sg.n + sg.count; ++n) {
-                const int row = quad < 4 ? tile0(n) + quad * 4 : tile1(n) + quad * 4 - 16;
-                const int lim = ep.gated && quad < 4 ? F : a.N;
-                float bv[4] = {};
-                if (bias) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (row + i < lim) bv[i] = h2f(__ldg(bias + row + i));
-                }
                 mbar_wait_or_abort(&rfull[b], ph, abort);
                 __syncwarp();
                 const uint32_t slot = sbase + (uint32_t)(L.part() + b * L.part_stride() + quad * 16);
-#pragma unroll
-                for (int it = 0; it < 2; ++it) {
-                    if (it * 4 >= sg.nr) break;
-                    const int m = it * 4 + (lane >> 3), mm = min(m, sg.nr - 1);
-                    const bool store = m < sg.nr && (!ep.gated || quad < 4);
-                    float y[4] = {}, res[4] = {};
-                    if (ep.residual && store) {
+                const int lim = ep.gated && quad < 4 ? F : a.N;
+                // (not unrolled, here and in the other rare paths: the roles share the instruction cache, and
+                // what they fetch anew for every unit shows: 61 -> 55 us on 64 experts of 3 rows)
+#pragma unroll 1
+                for (int p = 0; p < RS; ++p) {
+                    const int row = quad < 4 ? tile0(n, p) + quad * 4 : tile1(n, p) + quad * 4 - 16;
+                    float bv[4] = {};
+                    if (bias) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (row + i < lim) res[i] = h2f(ep.residual[(size_t)(sg.r0 + m) * ep.ldr + row + i]);
+                            if (row + i < lim) bv[i] = h2f(__ldg(bias + row + i));
                     }
+#pragma unroll 1
+                    for (int it = 0; it * 4 < sg.nr; ++it) {
+                        const int m = it * 4 + (lane >> 3), mm = min(m, sg.nr - 1);
+                        const bool store = m < sg.nr && (!ep.gated || quad < 4);
+                        float y[4] = {}, res[4] = {};
+                        if (ep.residual && store) {
 #pragma unroll
-                    for (int w = 0; w < kDecConsumers; ++w) {
-                        const uint4 v = lds128(slot + (uint32_t)((w * a.mc + mm) * kDecPartPitch * 4));
-                        y[0] += __uint_as_float(v.x), y[1] += __uint_as_float(v.y);
-                        y[2] += __uint_as_float(v.z), y[3] += __uint_as_float(v.w);
-                    }
-                    float other[4];
+                            for (int i = 0; i < 4; ++i)
+                                if (row + i < lim) res[i] = h2f(ep.residual[(size_t)(sg.r0 + m) * ep.ldr + row + i]);
+                        }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[i] += bv[i];
-                        other[i] = __shfl_down_sync(0xffffffffu, y[i], 4);
-                    }
-                    apply_act(y, ep.act);
-                    uint16_t* yp = ep.Y + (size_t)(sg.r0 + m) * ep.ldy + row;
+                        for (int w = 0; w < KS; ++w) {
+                            const uint4 v = lds128(slot + (uint32_t)(((p * KS + w) * a.mc + mm) * kDecPartPitch * 4));
+                            y[0] += __uint_as_float(v.x), y[1] += __uint_as_float(v.y);
+                            y[2] += __uint_as_float(v.z), y[3] += __uint_as_float(v.w);
+                        }
+                        float other[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (ep.gated) y[i] *= other[i];
-                        if (store && row + i < lim) yp[i] = f2h_rn(y[i] + res[i]);
+                        for (int i = 0; i < 4; ++i) {
+                            y[i] += bv[i];
+                            other[i] = __shfl_down_sync(0xffffffffu, y[i], 4);
+                        }
+                        apply_act(y, ep.act);
+                        uint16_t* yp = ep.Y + (size_t)(sg.r0 + m) * ep.ldy + row;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (ep.gated) y[i] *= other[i];
+                            if (store && row + i < lim) yp[i] = f2h_rn(y[i] + res[i]);
+                        }
                     }
                 }
                 __syncwarp();
@@ -358,10 +379,12 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     const int pitch = L.x_pitch();
     uint8_t* xs = smem + L.x();
     float* xsum = reinterpret_cast<float*>(smem + L.xsum());
-    // weights: row r of a tile, block b of 128 codes: [b][r][64 bytes]; this warp's block is cw
-    const uint32_t wofs = (uint32_t)(cw * 1024 + g * 64 + t * WT * 4);
-    const uint32_t cofs = smem_u32(smem + L.cvt()) + (uint32_t)(g * L.cvt_pitch() + (cw * 128 / G) * 8);
-    const uint32_t crow8 = 8u * L.cvt_pitch(), cstage = (uint32_t)(kDecRows * L.cvt_pitch());
+    const int part = cw / KS, ks = cw % KS;         // part of the unit, block of 128 codes of a stage
+    // weights: row r of a tile, block b of 128 codes: [b][r][64 bytes]
+    const uint32_t wofs = (uint32_t)(part * kSub + ks * 1024 + g * 64 + t * WT * 4);
+    const uint32_t cofs =
+        smem_u32(smem + L.cvt()) + (uint32_t)((part * kDecRows + g) * L.cvt_pitch() + (ks * 128 / G) * 8);
+    const uint32_t crow8 = 8u * L.cvt_pitch(), cstage = (uint32_t)(RS * kDecRows * L.cvt_pitch());
     const int m0 = 2 * t, m1 = 2 * t + 1;
     int st = 0, b = 0;
     uint32_t ph = 0, rph = 0;
@@ -373,7 +396,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         // that do not exist; per-k-step sums of x
         asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory");       // the previous segment's X is done with
         {
-            const int kwp = L.Kp >> 3, kwv = a.K >> 3;                 // kwp is a multiple of 256
+            const int kwp = L.Kp >> 3, kwv = a.K >> 3;                 // kwp is a multiple of 128
             constexpr int kBatch = 4;                                  // rows whose loads are in flight together
 #pragma unroll 1
             for (int mb = 0; mb < sg.nr; mb += kBatch) {
@@ -411,9 +434,9 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         }
         asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory");
         // lanes whose column is no row of X read row 0; their sums are not stored
-        const uint32_t xrow = smem_u32(xs + (g < sg.nr ? g : 0) * pitch) + (uint32_t)(t * 16 + cw * Q * WT * 64);
-        const uint32_t xs0 = smem_u32(xsum + (m0 < sg.nr ? m0 : 0) * L.nsteps + cw * Q);
-        const uint32_t xs1 = smem_u32(xsum + (m1 < sg.nr ? m1 : 0) * L.nsteps + cw * Q);
+        const uint32_t xrow = smem_u32(xs + (g < sg.nr ? g : 0) * pitch) + (uint32_t)(t * 16 + ks * Q * WT * 64);
+        const uint32_t xs0 = smem_u32(xsum + (m0 < sg.nr ? m0 : 0) * L.nsteps + ks * Q);
+        const uint32_t xs1 = smem_u32(xsum + (m1 < sg.nr ? m1 : 0) * L.nsteps + ks * Q);
         for (int n = 0; n < sg.count; ++n) {
             float y[2][4] = {};
             for (int c = 0; c < nchunks; ++c) {
@@ -421,17 +444,17 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
                 __syncwarp();
                 const uint32_t wb = sbase + (uint32_t)(st * kDecStageBytes) + wofs;
                 const uint32_t cv = cofs + (uint32_t)st * cstage;
-                const uint32_t xb = xrow + (uint32_t)(c * (kDecKC / kStepCodes) * WT * 64);
-                const uint32_t x0b = xs0 + (uint32_t)(c * (kDecKC / kStepCodes) * 4);
-                const uint32_t x1b = xs1 + (uint32_t)(c * (kDecKC / kStepCodes) * 4);
+                const uint32_t xb = xrow + (uint32_t)(c * (KC / kStepCodes) * WT * 64);
+                const uint32_t x0b = xs0 + (uint32_t)(c * (KC / kStepCodes) * 4);
+                const uint32_t x1b = xs1 + (uint32_t)(c * (KC / kStepCodes) * 4);
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
                     uint32_t wa[2][WT], wc[2][WT];
                     float d1[2][4], d16[2][4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        lds_words<WT>(wb + h * (kDecStageBytes / 2) + q * WT * 16, wa[h]);
-                        lds_words<WT>(wb + h * (kDecStageBytes / 2) + 512 + q * WT * 16, wc[h]);
+                        lds_words<WT>(wb + h * (kSub / 2) + q * WT * 16, wa[h]);
+                        lds_words<WT>(wb + h * (kSub / 2) + 512 + q * WT * 16, wc[h]);
                     }
 #pragma unroll
                     for (int j = 0; j < WT; ++j) {
@@ -497,32 +520,33 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
 
 // Rows of X at a time and stages that fit in `smem` bytes: as many rows as there are, up to 8, with
 // at least two stages.  false if not even one row fits.
-inline bool dec_plan(int rows, int K, int G, int smem, int& mc, int& S) {
+inline bool dec_plan(int rows, int K, int G, int RS, int smem, int& mc, int& S) {
     for (mc = std::min(rows, kDecMaxRows); mc >= 1; --mc)
         for (S = 6; S >= 2; --S)
-            if (DecSmem(mc, K, G, S).bytes() <= smem) return true;
+            if (DecSmem(mc, K, G, S, RS).bytes() <= smem) return true;
     return false;
 }
 
-inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d, int mc, int S, cudaStream_t st) {
+inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d, int RS, int mc, int S,
+                                       cudaStream_t st) {
     CUtensorMap tq;
     if (!make_tmap_3d(&tq, l.qweight, CU_TENSOR_MAP_DATA_TYPE_UINT32, 16, (uint64_t)l.E * l.N, (uint64_t)(l.K / 128),
-                      (uint64_t)l.K / 2, 64, 16, 16, kDecKC / 128))
+                      (uint64_t)l.K / 2, 64, 16, 16, 2048 / RS / 128))
         return AWQ_ERR_CUDA;
-    const void* fn = l.G == 32    ? (const void*)linear_decode_kernel<32>
-                     : l.G == 64  ? (const void*)linear_decode_kernel<64>
-                     : l.G == 128 ? (const void*)linear_decode_kernel<128>
-                                  : (const void*)linear_decode_kernel<256>;
+    const void* fn = l.G == 32    ? (RS == 2 ? (const void*)linear_decode_kernel<32, 2> : (const void*)linear_decode_kernel<32, 1>)
+                     : l.G == 64  ? (RS == 2 ? (const void*)linear_decode_kernel<64, 2> : (const void*)linear_decode_kernel<64, 1>)
+                     : l.G == 128 ? (RS == 2 ? (const void*)linear_decode_kernel<128, 2> : (const void*)linear_decode_kernel<128, 1>)
+                                  : (const void*)linear_decode_kernel<256, 1>;
     if (!prepare_kernel(fn)) return AWQ_ERR_CUDA;
     DecArgs a = {l.X, l.ldx, l.scales, l.qzeros, l.rows, l.offsets, l.T, l.R, l.E, l.N, l.K, 0, mc, S, l.ep};
-    a.units = l.ep.gated ? ceil_div(l.N / 2, 16) : ceil_div(l.N, kDecRows);
+    a.units = l.ep.gated ? ceil_div(l.N / 2, 16 * RS) : ceil_div(l.N, 32 * RS);
     // (grouped: every expert with rows adds at most one partial set)
     const long long sets = l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc);
     const long long grid = std::min<long long>(d.sms, sets * a.units);
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)grid);
     lc.blockDim = dim3(kDecThreads);
-    lc.dynamicSmemBytes = DecSmem(mc, l.K, l.G, S).bytes();
+    lc.dynamicSmemBytes = DecSmem(mc, l.K, l.G, S, RS).bytes();
     lc.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -540,12 +564,15 @@ inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d,
 inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaStream_t st) {
     const int share = l.offsets ? ceil_div(l.R, std::min(l.R, l.E)) : l.R;
     int mc = 0, S = 0;
-    if (share <= kDecMaxRows && l.K % 128 == 0 && dec_plan(l.R, l.K, l.G, d.max_smem_optin, mc, S) &&
+    // 64-row units where every CTA gets many, however the units fall (and a stage has 8 groups per row)
+    const long long units = (long long)(l.offsets ? std::min(l.R, l.E) : 1) * ceil_div(l.ep.gated ? l.N / 2 : l.N, 32);
+    const int RS = l.G <= 128 && units >= (long long)kDecManyUnits * d.sms ? 2 : 1;
+    if (share <= kDecMaxRows && l.K % 128 == 0 && dec_plan(l.R, l.K, l.G, RS, d.max_smem_optin, mc, S) &&
         (mc >= share || (!l.offsets && 2 * mc >= share && (long long)l.N * l.K <= (128LL << 20)))) {
         // a CTA's list of segments must hold the row sets that its units may reach
         const long long sets = l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc);
         if (sets <= (long long)(kDecMaxSegs - 2) * d.sms && sets * ceil_div(l.N, 32) < 0x7fffffffLL)
-            return launch_linear_decode(l, d, mc, S, st);
+            return launch_linear_decode(l, d, RS, mc, S, st);
     }
     return launch_linear_tc(l, d.sms, st);
 }
