@@ -68,7 +68,8 @@ SIGNATURES = {
     "awq_linear_grouped": (ctypes.c_int, [_u16p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
                                           ctypes.c_void_p, ctypes.c_int32, _u32p, _u16p, _u32p, ctypes.c_int32,
                                           ctypes.c_int32, QuantConfig, _u16p, ctypes.c_int32, ctypes.c_int32, _u16p,
-                                          ctypes.c_int64, ctypes.c_void_p]),
+                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "awq_linear_grouped_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
     "awq_moe_route": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                      ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
@@ -442,16 +443,27 @@ def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bi
 
 
 _I32 = (torch.int32,)
+_GATHER_MIN_SHARE = 64   # rows per expert below which a grouped call asks for no workspace
+
+
+def _scratch(like: torch.Tensor, need: int, stream) -> torch.Tensor:
+    """Workspace of one call, freed on its return: not to be reused before `stream` has passed it."""
+    ws = like.new_empty(need, dtype=torch.uint8)
+    if stream is not None:
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                         else torch.cuda.ExternalStream(_stream(stream), device=like.device))
+    return ws
 
 
 def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=128, zero_point=True, bias=None,
-                   activation=None, gated=False, out=None, stream=None) -> torch.Tensor:
+                   activation=None, gated=False, out=None, workspace=None, stream=None) -> torch.Tensor:
     """awq_linear_grouped: the fused linear with one matrix per expert (qweight [E][N][K/8], scales
     [E][N][K/G], qzeros [E][N][..], bias [E][N]).  Rows offsets[e]..offsets[e+1]-1 of the result
     [R][N or N/2] use expert e; offsets is an int32 [E+1] CUDA tensor, never read by the host.
 
     Row p reads row rows[p] of X (int32 [R]; R = len(rows)), or row p where rows is None (R = len(X)).
-    Rows that no expert owns are left as they are in `out` (uninitialised without one)."""
+    Rows that no expert owns are left as they are in `out` (uninitialised without one).  Large gathered
+    calls copy their rows into a workspace first (allocated here unless one is given)."""
     dev = _cuda(X, "X")
     T, K = X.shape
     E = qweight.shape[0]
@@ -465,9 +477,14 @@ def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=12
         out = X.new_empty((R, n_out))
     px, ldx = _rows(X, "X", dev, T, K)
     py, ldy = _rows(out, "out", dev, R, n_out)
+    if workspace is None and R >= _GATHER_MIN_SHARE * E and rows is not None:
+        need = (_lib or load_library()).awq_linear_grouped_workspace_bytes(R, E, K)
+        if need:
+            workspace = _scratch(X, need, stream)
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _linear_grouped(dev, stream, px, T, ldx, _flat(rows, "rows", dev, (R,), _I32), R,
         _flat(offsets, "offsets", dev, (E + 1,), _I32), E, pq, ps, pz, N, K, _config(group_size, zero_point),
-        _flat(bias, "bias", dev, (E, N), _F16), act, 1 if gated else 0, py, ldy)
+        _flat(bias, "bias", dev, (E, N), _F16), act, 1 if gated else 0, py, ldy, ws, ws_bytes)
     return out
 
 
@@ -502,10 +519,7 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
     if workspace is None:
         need = _route_need(T, E, dev)
         if need:
-            workspace = logits.new_empty(need, dtype=torch.uint8)
-            if stream is not None:   # freed on return: not to be reused before `stream` has passed the kernels
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                        else torch.cuda.ExternalStream(_stream(stream), device=logits.device))
+            workspace = _scratch(logits, need, stream)
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _moe_route(dev, stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0,
         _flat(weights, "weights", dev, slots, _F32), _flat(experts, "experts", dev, slots, _I32),

@@ -321,7 +321,7 @@ awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uin
     if (M == 0) return AWQ_OK;
     const Epilogue ep = {bias, residual, (long long)ldr, Y, (long long)ldy, activation, gated};
     const LinearArgs l = {X, M, (long long)ldx, nullptr, M, nullptr, 1, qweight, scales,
-                          cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep};
+                          cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep, nullptr, 0};
     return run_linear(l, (cudaStream_t)stream);
 }
 
@@ -329,20 +329,23 @@ awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const i
                               const int32_t* offsets, int32_t E, const uint32_t* qweight, const uint16_t* scales,
                               const uint32_t* qzeros, int32_t N, int32_t K, awq_quant_config cfg,
                               const uint16_t* bias, int32_t activation, int32_t gated, uint16_t* Y, int64_t ldy,
-                              void* stream) {
+                              void* ws, size_t ws_bytes, void* stream) {
     awq_status st = check_fused(X, T, ldx, qweight, scales, qzeros, N, K, cfg, bias, activation, gated, nullptr, 0, Y,
                                 ldy, R == 0 || T == 0);
     if (st != AWQ_OK) return st;
     if (R < 0 || E < 1 || E > kRouteMaxExperts || !offsets || !aligned4(offsets) || !aligned4(rows))
         return AWQ_ERR_INVALID_ARG;
+    if (!aligned16(ws)) return AWQ_ERR_INVALID_ARG;
     if ((int64_t)E * N > 0x7ffffe00LL) return AWQ_ERR_UNSUPPORTED;
     if (R == 0) return AWQ_OK;
     if (T == 0 || !Y || (!rows && T < R)) return AWQ_ERR_INVALID_ARG;
     const Epilogue ep = {bias, nullptr, 0, Y, (long long)ldy, activation, gated};
     const LinearArgs l = {X, T, (long long)ldx, rows, R, offsets, E, qweight, scales,
-                          cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep};
+                          cfg.zero_point ? qzeros : nullptr, N, K, cfg.q_group_size, ep, ws, ws ? ws_bytes : 0};
     return run_linear(l, (cudaStream_t)stream);
 }
+
+size_t awq_linear_grouped_workspace_bytes(int32_t R, int32_t E, int32_t K) { return gather_workspace_bytes(R, E, K); }
 
 size_t awq_moe_route_workspace_bytes(int32_t T, int32_t E) {
     DeviceInfo d;

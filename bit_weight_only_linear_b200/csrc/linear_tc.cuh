@@ -656,9 +656,40 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
     }
 }
 
+// Copies the rows of X that the experts' rows name (zeros for numbers outside X) into `out` [R][K], so
+// that the tiles can read them in place.  A warp per row and pass; rows that no expert owns are left.
+constexpr int kGatherThreads = 256;
+
+__global__ void __launch_bounds__(kGatherThreads)
+gather_rows_kernel(const uint16_t* __restrict__ X, int T, long long ldx, const int32_t* __restrict__ rows, int R,
+                   const int32_t* __restrict__ offsets, int E, int K, uint16_t* __restrict__ out) {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int begin = min(max(__ldg(offsets), 0), R), end = min(max(__ldg(offsets + E), 0), R);
+    for (long long p = begin + (long long)blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5); p < end;
+         p += (long long)gridDim.x * (kGatherThreads / 32)) {
+        const int r = __ldg(rows + p);
+        const bool live = r >= 0 && r < T;
+        const uint4* src = reinterpret_cast<const uint4*>(X + (live ? r : 0) * ldx);
+        uint4* dst = reinterpret_cast<uint4*>(out + p * K);
+#pragma unroll 4
+        for (int i = lane; i < K / 8; i += 32) dst[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+
+// Rows per expert from which a gathered product first copies its rows in order: the copy costs 4 R K
+// bytes and a launch, the gathering producers hold the MMAs up (4096 tokens x 2 of 8 experts, 28672 x 4096:
+// 1758 us gathered in place).
+constexpr int kGatherMinShare = 64;
+
+inline size_t gather_workspace_bytes(int R, int E, int K) {
+    if (R <= 0 || E <= 0 || K <= 0 || (long long)R < (long long)kGatherMinShare * E) return 0;
+    return align256((size_t)R * K * 2);
+}
 
 struct LinearArgs {
     const uint16_t* X;
@@ -673,6 +704,8 @@ struct LinearArgs {
     const uint32_t* qzeros;      // NULL: implicit zero 8
     int N, K, G;
     Epilogue ep;
+    void* ws;                    // gather_workspace_bytes(), or NULL: rows are gathered in place
+    size_t ws_bytes;
 };
 
 inline bool make_tmap_ld(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t rows, uint64_t cols,
@@ -800,6 +833,22 @@ inline awq_status launch_linear_tc(const LinearArgs& l, int sms, cudaStream_t st
         if (m <= 32) return launch_tc_bn<32>(l, 1, st);
         return launch_tc_bn<64>(l, 1, st);
     }
+    LinearArgs in_place = l;
+    if (l.rows && l.offsets && l.ws) {
+        const size_t need = gather_workspace_bytes(l.R, l.E, l.K);
+        if (need && l.ws_bytes >= need) {
+            uint16_t* out = static_cast<uint16_t*>(l.ws);
+            void* args[] = {&in_place.X, &in_place.T, &in_place.ldx, &in_place.rows, &in_place.R,
+                            &in_place.offsets, &in_place.E, &in_place.K, &out};
+            const long long blocks = std::min<long long>(8LL * sms, ceil_div(l.R, kGatherThreads / 32));
+            if (!launch_pdl((const void*)gather_rows_kernel, dim3((unsigned)blocks), dim3(kGatherThreads), args, st))
+                return AWQ_ERR_CUDA;
+            in_place.X = out;
+            in_place.T = l.R;
+            in_place.ldx = l.K;
+            in_place.rows = nullptr;
+        }
+    }
     int best = 1;
     bool wide = false;
     double best_t = 1e30;
@@ -811,7 +860,7 @@ inline awq_status launch_linear_tc(const LinearArgs& l, int sms, cudaStream_t st
             if (t < best_t) best_t = t, best = s, wide = w;
         }
     }
-    return wide ? launch_tc_bn<192>(l, best, st) : launch_tc_bn<128>(l, best, st);
+    return wide ? launch_tc_bn<192>(in_place, best, st) : launch_tc_bn<128>(in_place, best, st);
 }
 
 }  // namespace awq

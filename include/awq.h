@@ -262,12 +262,18 @@ awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uin
  * values at capture.  Entries beyond the limits never read or write out of bounds: offsets
  * are clamped to 0 .. R, and a row number outside 0 .. T-1 counts as a row of zeros.
  * 1 <= E <= 1024, R >= 0 (0 does nothing).
+ * ws: with rows, awq_linear_grouped_workspace_bytes(R, E, K) bytes let a large call copy its rows
+ * together first, which is faster; NULL (or too small) only does without.  Not to be used by two calls
+ * at once.
  */
 awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const int32_t* rows, int32_t R,
                               const int32_t* offsets, int32_t E, const uint32_t* qweight,
                               const uint16_t* scales, const uint32_t* qzeros, int32_t N, int32_t K,
                               awq_quant_config cfg, const uint16_t* bias, int32_t activation, int32_t gated,
-                              uint16_t* Y, int64_t ldy, void* stream);
+                              uint16_t* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes with which awq_linear_grouped copies gathered rows together first (0: it does not). */
+size_t awq_linear_grouped_workspace_bytes(int32_t R, int32_t E, int32_t K);
 
 /* Scores of awq_moe_route: softmax over all experts of a token, or sigmoid of each. */
 enum { AWQ_SCORE_SOFTMAX = 0, AWQ_SCORE_SIGMOID = 1 };

@@ -247,6 +247,24 @@ def test_linear_grouped_bad_tables_stay_in_bounds(lib, n_rows):
         assert torch.isnan(buf).all()
 
 
+@pytest.mark.parametrize("ws", ["own", "none", "short", "given"])
+def test_linear_grouped_gather_workspace(lib, ws):
+    """Many gathered rows: with the copy into a workspace and without, rows outside X zero in both."""
+    counts, N, K, G, E = [150, 0, 131, 90], 258, 512, 64, 4
+    w, X, _, rows, offsets, n_rows = _grouped(77, counts, N, K, G, True, "silu", True, False, True, T=60, gap=5)
+    rows[7], rows[160], rows[n_rows - 6] = -3, 60, 2 ** 30
+    y = torch.full((n_rows, N // 2), NAN, dtype=torch.float16, device="cuda")
+    kw = {}
+    if ws != "own":
+        size = {"none": 0, "short": n_rows * K * 2 - 256, "given": n_rows * K * 2 + 256}[ws]
+        kw = dict(workspace=torch.full((size,), 255, dtype=torch.uint8, device="cuda"))
+    lib.linear_grouped(X, *w, offsets, rows, G, True, activation="silu", gated=True, out=y, **kw)
+    _finish(lib)
+    X0 = torch.cat((X, torch.zeros(1, K, dtype=torch.float16, device="cuda")))
+    _check_grouped(y, X0, w, G, None, torch.where((rows < 0) | (rows >= 60), 60, rows), offsets, "silu", True)
+    assert torch.isnan(y[:5]).all() and torch.isnan(y[n_rows - 5:]).all()
+
+
 def test_linear_grouped_equals_the_dense_product(lib):
     """One expert with every row is linear_fused."""
     for M in (1, 5, 8, 20, 100, 400):

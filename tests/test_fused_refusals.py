@@ -29,10 +29,11 @@ def _fused(clib, **kw):
 
 def _grouped(clib, **kw):
     a = dict(X=FAKE, T=4, ldx=256, rows=0, R=4, o=FAKE, E=3, q=FAKE, s=FAKE, z=FAKE, N=64, K=256, c=_cfg(), b=0, act=0,
-             gated=0, Y=FAKE, ldy=64)
+             gated=0, Y=FAKE, ldy=64, ws=0, wb=0)
     a.update(kw)
     return clib.awq_linear_grouped(a["X"], a["T"], a["ldx"], a["rows"], a["R"], a["o"], a["E"], a["q"], a["s"], a["z"],
-                                   a["N"], a["K"], a["c"], a["b"], a["act"], a["gated"], a["Y"], a["ldy"], None)
+                                   a["N"], a["K"], a["c"], a["b"], a["act"], a["gated"], a["Y"], a["ldy"],
+                                   a["ws"], a["wb"], None)
 
 
 @pytest.mark.parametrize("call", [_fused, _grouped])
@@ -66,6 +67,10 @@ def test_grouped_only(clib):
     assert _grouped(clib, rows=FAKE + 2) == INVALID
     assert _grouped(clib, R=5) == INVALID                       # rows of X missing
     assert _grouped(clib, T=0, rows=FAKE) == INVALID
+    assert _grouped(clib, ws=FAKE + 8, wb=1 << 20) == INVALID
+    assert clib.awq_linear_grouped_workspace_bytes(100, 8, 4096) == 0          # few rows are gathered in place
+    assert clib.awq_linear_grouped_workspace_bytes(8000, 8, 4096) == 8000 * 8192
+    assert clib.awq_linear_grouped_workspace_bytes(-1, 8, 4096) == 0
     assert _grouped(clib, E=1024, N=1 << 22, ldy=1 << 22) == UNSUPPORTED
     assert _grouped(clib, R=0, T=0, X=0, Y=0) == OK
 
