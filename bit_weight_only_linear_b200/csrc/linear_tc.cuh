@@ -368,14 +368,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             int s = 0, b = 0;
             uint32_t xph = 0, aph = 0;
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait(&xfull[s], xph)) break;
+                mbar_wait_or_abort(&xfull[s], xph, &misc[5]);
                 if (a.rows) fence_proxy_async_smem();
                 const uint64_t bdesc = bdesc0 + (uint64_t)(s * (C::kXBytes >> 4));
-                bool ok = true;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ok = ok && mbar_wait(&afull[2 * b + h], aph);
-                    if (!ok) break;
+                    mbar_wait_or_abort(&afull[2 * b + h], aph, &misc[5]);
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kGemmKB / 16; ++kk)
@@ -383,7 +381,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                                    (kb | kk) != 0);
                     mma_commit(&aempty[2 * b + h]);
                 }
-                if (!ok) break;
                 mma_commit(&xempty[s]);
                 if (++s == C::kXStages) s = 0, xph ^= 1u;
                 if (++b == C::kABufs) b = 0, aph ^= 1u;
@@ -443,7 +440,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         const uint32_t wline = smem_u32(smem + C::kWOff) + (uint32_t)(h * (C::kWBytes / 2) + r * 128 + (r & 7) * 16);
         const uint32_t part_x = (uint32_t)(part0 * 16);
         const uint32_t aline = abase + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 32 + part0 * 16);
-        const uint32_t af = smem_u32(afull + h), ae = smem_u32(aempty + h);
+        const uint32_t af = smem_u32(afull + h), ae = smem_u32(aempty + h), abort = smem_u32(&misc[5]);
         int ws = 0;
         uint32_t wph = 0, aph = 1;
 #pragma unroll 1
@@ -492,8 +489,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                     if (i == 0) {
                         // use number (kb + sb) / kABufs of the buffer
                         const uint32_t parity = C::kABufs == kTcWKB ? aph : (uint32_t)(((sb / C::kABufs) & 1) ^ 1);
-                        if (!mbar_try_wait(ae + b * 16, parity))
-                            mbar_wait_or_abort(&aempty[2 * b + h], parity, &misc[5]);
+                        mbar_wait_or_abort(ae + b * 16, parity, abort);
                         __syncwarp();
                         tc_fence_after();
                     }
