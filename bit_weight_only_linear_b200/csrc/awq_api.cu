@@ -276,6 +276,10 @@ awq_status awq_scale_search_noalloc(const uint16_t* X, int32_t M, const uint16_t
 
 namespace {
 
+// Rows of X and weight rows (of all experts) that the kernels' 32-bit indexes and tile coordinates hold.
+constexpr int kFusedMaxRows = 1 << 30;
+constexpr int kFusedMaxN = 0x7ffffe00;
+
 // Checks shared by the fused and the grouped linear; the row counts may be 0.
 awq_status check_fused(const uint16_t* X, int M, int64_t ldx, const uint32_t* qweight, const uint16_t* scales,
                        const uint32_t* qzeros, int N, int K, const awq_quant_config& cfg, const uint16_t* bias,
@@ -287,6 +291,7 @@ awq_status check_fused(const uint16_t* X, int M, int64_t ldx, const uint32_t* qw
     if (st != AWQ_OK) return st;
     if (M < 0 || activation < AWQ_ACT_NONE || activation > AWQ_ACT_GELU_TANH || (gated != 0 && gated != 1))
         return AWQ_ERR_INVALID_ARG;
+    if (M > kFusedMaxRows || N > kFusedMaxN) return AWQ_ERR_UNSUPPORTED;
     if (gated && (N & 1)) return AWQ_ERR_INVALID_ARG;
     const int64_t n_out = gated ? N / 2 : N;
     if (ldx < K || (ldx & 7) || ldy < n_out || (residual && ldr < n_out)) return AWQ_ERR_INVALID_ARG;
@@ -336,7 +341,7 @@ awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const i
     if (R < 0 || E < 1 || E > kRouteMaxExperts || !offsets || !aligned4(offsets) || !aligned4(rows))
         return AWQ_ERR_INVALID_ARG;
     if (!aligned16(ws)) return AWQ_ERR_INVALID_ARG;
-    if ((int64_t)E * N > 0x7ffffe00LL) return AWQ_ERR_UNSUPPORTED;
+    if ((int64_t)E * N > kFusedMaxN || R > kFusedMaxRows) return AWQ_ERR_UNSUPPORTED;
     if (R == 0) return AWQ_OK;
     if (T == 0 || !Y || (!rows && T < R)) return AWQ_ERR_INVALID_ARG;
     const Epilogue ep = {bias, nullptr, 0, Y, (long long)ldy, activation, gated};

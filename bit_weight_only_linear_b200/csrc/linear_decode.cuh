@@ -171,7 +171,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     DecSeg* segs = reinterpret_cast<DecSeg*>(smem + L.segs());
     if (warp == 1) {
         // this CTA's share of all row sets' units, as segments
-        const long long total = (long long)dec_sets(a) * a.units;
+        const long long total = min((long long)dec_sets(a) * a.units, 0x7fffffffLL);
         const int u_begin = (int)(total * blockIdx.x / gridDim.x), u_end = (int)(total * (blockIdx.x + 1) / gridDim.x);
         int count = 0;
         for (int u = u_begin; u < u_end && count < kDecMaxSegs; ++count) {
@@ -558,20 +558,25 @@ inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d,
 }
 
 // Which form takes a call.  The decode form takes up to 8 rows a matrix and whole 128-code blocks; above
-// that the tensor-core tiles win.  Where X's rows do not all fit in shared memory it needs a second pass
-// over the weights, which pays while that comes from L2 (8 rows x 14336, 4096 channels: 20 us against 22 for
-// the tiles; 3 rows x 28672, 8192 channels, 117 MB: 61 us against 48).
+// that the tensor-core tiles win.  A dense batch may also take two passes over the weights, which pays while
+// the second comes from L2 and X leaves room for a ring: 16 rows x 4096, 28672 channels 26 us against 29 for
+// the tiles, 4096 channels 8.7 against 10.1; 8 rows x 14336 20 against 22.  It does not where weights are
+// many (3 rows x 28672, 8192 channels: 61 against 48) or X is wide (16 rows x 14336: 32 against 21).
 inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaStream_t st) {
     const int share = l.offsets ? ceil_div(l.R, std::min(l.R, l.E)) : l.R;
-    int mc = 0, S = 0;
     // 64-row units where every CTA gets many, however the units fall (and a stage has 8 groups per row)
     const long long units = (long long)(l.offsets ? std::min(l.R, l.E) : 1) * ceil_div(l.ep.gated ? l.N / 2 : l.N, 32);
     const int RS = l.G <= 128 && units >= (long long)kDecManyUnits * d.sms ? 2 : 1;
-    if (share <= kDecMaxRows && l.K % 128 == 0 && dec_plan(l.R, l.K, l.G, RS, d.max_smem_optin, mc, S) &&
-        (mc >= share || (!l.offsets && 2 * mc >= share && (long long)l.N * l.K <= (128LL << 20)))) {
+    const int passes = l.offsets || share <= 1 || (long long)l.N * l.K > (128LL << 20) ? 1 : 2;
+    if (share <= kDecMaxRows * passes && l.K % 128 == 0) {
+        int mc = 0, S = 0;
+        bool fits = dec_plan(l.R, l.K, l.G, RS, d.max_smem_optin, mc, S) && mc >= share;
+        if (!fits && passes == 2)
+            fits = dec_plan(ceil_div(share, 2), l.K, l.G, RS, d.max_smem_optin, mc, S) && 2 * mc >= share &&
+                   (share <= kDecMaxRows || S >= 3);
         // a CTA's list of segments must hold the row sets that its units may reach
-        const long long sets = l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc);
-        if (sets <= (long long)(kDecMaxSegs - 2) * d.sms && sets * ceil_div(l.N, 32) < 0x7fffffffLL)
+        const long long sets = !fits ? 0 : (l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc));
+        if (fits && sets <= (long long)(kDecMaxSegs - 2) * d.sms && sets * ceil_div(l.N, 32) < 0x7fffffffLL)
             return launch_linear_decode(l, d, RS, mc, S, st);
     }
     return launch_linear_tc(l, d.sms, st);

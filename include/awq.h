@@ -244,7 +244,11 @@ enum {
  * not overlap any other input.  Rows may be strided: ldx, ldr, ldy are the distances of
  * rows in elements; ldx a multiple of 8 (X 16-byte aligned as ever), while bias, residual
  * and Y need only their element's alignment.  N need not be a multiple of anything.
- * Needs no workspace.  Range: as awq_linear_gemm when M > 8 (AWQ_ERR_RANGE).
+ * Needs no workspace.  Range: a batch on the tensor-core tiles (always above 16 rows) rounds each
+ * dequantised weight once to fp16 and reports AWQ_ERR_RANGE as awq_linear_gemm does; calls of few rows
+ * multiply codes and scales exactly and have no such limit.
+ * Ordering: as awq_linear_gemv, a call may read the weights before the previous kernel on `stream` has
+ * completed, so that kernel must not write them (the quantisers end with an ordering kernel of theirs).
  */
 awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uint32_t* qweight,
                             const uint16_t* scales, const uint32_t* qzeros, int32_t N, int32_t K,

@@ -1,6 +1,9 @@
 """GPU: the fused linear, the expert-grouped linear, routing and combination against plain fp64
 implementations (tests/fused_reference.py derives the bounds)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -30,6 +33,9 @@ LINEAR = [
     (8, 1022, 4096, 32, True, "silu", True, False, True),
     (8, 96, 14336, 256, True, None, False, False, False),
     (9, 257, 160, 32, True, "silu", False, True, True),
+    (9, 260, 4096, 128, True, "silu", True, False, True),
+    (15, 1030, 2048, 64, False, None, False, True, True),
+    (16, 512, 8192, 256, True, "relu", True, True, False),
     (16, 4096, 4096, 128, True, None, False, False, True),
     (17, 700, 1024, 64, False, "gelu", True, True, True),
     (31, 384, 4096, 256, True, "relu", True, False, False),
@@ -119,15 +125,20 @@ def test_linear_fused_overflow_to_inf(lib):
 
 
 def test_linear_fused_range_flag(lib):
-    """Weights beyond fp16 are flagged, as in linear_gemm."""
+    """More than 16 rows: weights beyond fp16 are flagged, as in linear_gemm.  Few rows: they multiply
+    in fp32 exactly, without a limit (K a multiple of 128)."""
     N, K, G = 64, 128, 128
     q, s, z = R.packed(40, N, K, G, True)
-    X = torch.full((16, K), 60000.0, dtype=torch.float16, device="cuda")
-    lib.linear_fused(X, torch.full_like(q, -1), torch.full_like(s, 60000.0), torch.zeros_like(z), G, True)
+    big = (torch.full_like(q, -1), torch.full_like(s, 60000.0), torch.zeros_like(z))
+    lib.linear_fused(torch.full((17, K), 2.0 ** -10, dtype=torch.float16, device="cuda"), *big, G, True)
     with pytest.raises(lib.AWQError) as e:
         lib.device_error()
     assert e.value.status == lib.AWQ_ERR_RANGE
     lib.device_error()
+    y = lib.linear_fused(torch.full((8, K), 2.0 ** -14, dtype=torch.float16, device="cuda"), *big, G, True)
+    _finish(lib)
+    want = 2.0 ** -14 * 15 * 60000 * K          # 7031.25
+    assert ((y.double() - want).abs() <= R.HALF * want * 1.01).all()
 
 
 def test_linear_fused_agrees_with_linear_gemm(lib):
@@ -480,6 +491,40 @@ def test_moe_layer_captured_and_replayed(lib, T):
         lib.device_error()
         for i in range(2):
             assert torch.equal(outs[i], eager[i][1 - i if swap else i])
+
+
+FIRST_CALL = """
+import sys; sys.path[:0] = ["tests", "."]
+import torch
+import fused_reference as R
+from bit_weight_only_linear_b200 import awq
+w = [R.packed(1, 256, 1024, 128, True), R.packed(2, 256, 1024, 128, True, lead=(4,))]
+X = {m: R.activations(m, m, 1024) for m in (2, 61, 300)}
+logits = {m: torch.randn(m, 4, generator=torch.Generator().manual_seed(m)).cuda() for m in X}
+def calls(m):
+    r = awq.moe_route(logits[m], 2)
+    h = awq.linear_grouped(X[m], *w[1], r.offsets, r.rows, 128, True)
+    return [awq.linear_fused(X[m], *w[0], 128, True), awq.moe_combine(h, r.weights, r.positions)]
+torch.cuda.synchronize()
+outs = {}
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for m in X:
+        outs[m] = calls(m)
+g.replay()
+torch.cuda.synchronize()
+awq.device_error()
+for m in X:
+    assert all(torch.equal(a, b) for a, b in zip(outs[m], calls(m))), m
+print("captured")
+"""
+
+
+def test_first_calls_inside_a_capture(lib):
+    """A process whose first call of every form is a captured one."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_dense_mlp_on_a_side_stream(lib):

@@ -55,6 +55,8 @@ def test_fused_only(clib):
     assert _fused(clib, r=FAKE, ldr=63) == INVALID
     assert _fused(clib, r=FAKE + 1, ldr=64) == INVALID
     assert _fused(clib, M=0, X=0, Y=0) == OK
+    assert _fused(clib, M=(1 << 30) + 1) == UNSUPPORTED
+    assert _fused(clib, N=0x7ffffe01, ldy=0x7ffffe01) == UNSUPPORTED
 
 
 def test_grouped_only(clib):
@@ -72,6 +74,7 @@ def test_grouped_only(clib):
     assert clib.awq_linear_grouped_workspace_bytes(8000, 8, 4096) == 8000 * 8192
     assert clib.awq_linear_grouped_workspace_bytes(-1, 8, 4096) == 0
     assert _grouped(clib, E=1024, N=1 << 22, ldy=1 << 22) == UNSUPPORTED
+    assert _grouped(clib, R=(1 << 30) + 1, T=1 << 30, rows=FAKE) == UNSUPPORTED
     assert _grouped(clib, R=0, T=0, X=0, Y=0) == OK
 
 
