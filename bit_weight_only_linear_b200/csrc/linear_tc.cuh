@@ -21,6 +21,11 @@
 //     distributed shared memory and are added in rank order (no workspace, no second kernel).
 //   * Grouped: every expert's rows are cut into tiles of their own; a CTA finds its tile by a scan
 //     over the offsets table, so nothing is read back to the host.
+// Bound: the tensor cores from about 150 rows on (2048 rows x 57344 x 8192, gated: 1.33 ms = 1450 TFLOP/s,
+// 0.87 of the measured burst rate, above the sustained one); the round trip between conversion and MMA,
+// 0.3 us per 64 codes of 256 rows, below (61 rows x 4096 x 14336: 24 us, of which 8 are the start and the
+// exchange of the splits); with 16 rows a tile the issue of the conversion (96 tokens, 6 of 64 experts, 2816 x
+// 2048: 71 us = 2.8 TB/s).
 // Each dequantised weight is rounded once to fp16, as in awq_linear_gemm, whose range flag it
 // raises too.  Every wait is bounded: on time-out the kernel raises the device error word, drains
 // what it issued, frees TMEM and returns.
@@ -679,7 +684,7 @@ gather_rows_kernel(const uint16_t* __restrict__ X, int T, long long ldx, const i
 
 // Rows per expert from which a gathered product first copies its rows in order: the copy costs 4 R K
 // bytes and a launch, the gathering producers hold the MMAs up (4096 tokens x 2 of 8 experts, 28672 x 4096:
-// 1758 us gathered in place).
+// 1758 us gathered in place, 1530 copied first; 64 rows an expert 253 and 211).
 constexpr int kGatherMinShare = 64;
 
 inline size_t gather_workspace_bytes(int R, int E, int K) {

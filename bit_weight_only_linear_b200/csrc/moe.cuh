@@ -11,10 +11,12 @@
 //     bits in the expert's mask (the masks are built by atomicOr, whose result does not depend on
 //     order).  Blocks take contiguous ranges of tokens and publish their counts; the second kernel
 //     adds the counts of the blocks before its own.  One block needs no second kernel.
-// Bound: a launch's latency for decode; for a long prefill the issue of the top_k rounds.
+// Bound: a launch's latency for decode (8 tokens, 8 experts: 3.7 us); for a long prefill the latency of the
+// walks and of the second launch (16384 tokens, top 8 of 128, fp16: 24 us).
 //
 // Combination.  out[t] = residual[t] + sum_j w[t][j] Y[positions[t][j]], fp32 sums in slot order,
-// one rounding: bound by reading the T top_k rows once.
+// one rounding: bound by reading the T top_k rows once (8192 tokens x 8 x 4096: 103 us = 6.46 TB/s, 0.99 of the
+// measured copy rate).
 #pragma once
 
 #include "common.cuh"
