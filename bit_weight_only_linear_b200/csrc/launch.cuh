@@ -60,19 +60,4 @@ inline bool kernel_occupancy(const void* fn, int threads, size_t smem, int& occ)
     return true;
 }
 
-// Launch as a programmatic dependent of the stream's previous kernel (every kernel launched so waits
-// for it before it touches global memory).
-inline bool launch_pdl(const void* fn, dim3 grid, dim3 block, void** args, cudaStream_t st) {
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = grid;
-    lc.blockDim = block;
-    lc.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess;
-}
-
 }  // namespace awq

@@ -29,6 +29,7 @@
 #include "epilogue.cuh"
 #include "gemv.cuh"
 #include "gemv_launch.cuh"
+#include "linear_common.cuh"
 #include "linear_tc.cuh"
 #include "sm100.cuh"
 

@@ -40,6 +40,7 @@
 #include "gemm_sm100.cuh"
 #include "gemv.cuh"
 #include "launch.cuh"
+#include "linear_common.cuh"
 #include "sm100.cuh"
 
 namespace awq {

@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "gemv_launch.cuh"
+#include "linear_common.cuh"
 
 namespace awq {
 
