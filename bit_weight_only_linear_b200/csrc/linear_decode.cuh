@@ -44,6 +44,7 @@ constexpr int kDecStageBytes = 32 * 1024;        // 32 RS rows x 2048 / RS codes
 constexpr int kDecMaxRows = 8;                   // rows of X at a time (MMA N)
 constexpr int kDecManyUnits = 8;                 // 32-row units per CTA from which a unit is 64 rows
 constexpr int kDecMaxSegs = 32;                  // segments of a CTA
+constexpr int kDecMaxK = 1 << 17;                // (no row of X beyond it fits in shared memory)
 constexpr int kDecPartPitch = 36;                // words per row of X in a partial sum (bank spread)
 
 struct DecSmem {
@@ -572,7 +573,7 @@ inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaSt
     const long long units = (long long)(l.offsets ? std::min(l.R, l.E) : 1) * ceil_div(l.ep.gated ? l.N / 2 : l.N, 32);
     const int RS = l.G <= 128 && units >= (long long)kDecManyUnits * d.sms ? 2 : 1;
     const int passes = l.offsets || share <= 1 || (long long)l.N * l.K > (128LL << 20) ? 1 : 2;
-    if (share <= kDecMaxRows * passes && l.K % 128 == 0) {
+    if (share <= kDecMaxRows * passes && l.K % 128 == 0 && l.K <= kDecMaxK) {
         int mc = 0, S = 0;
         bool fits = dec_plan(l.R, l.K, l.G, RS, d.max_smem_optin, mc, S) && mc >= share;
         if (!fits && passes == 2)

@@ -19,6 +19,8 @@
 // measured copy rate).
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "gemv_launch.cuh"
 #include "linear_common.cuh"
@@ -459,7 +461,7 @@ inline int route_blocks(int T, int sms, int& per_block) {
         per_block = ceil_div(T, 32) * 32;
         return 1;
     }
-    per_block = ceil_div(ceil_div(T, sms), 32) * 32;
+    per_block = std::min(ceil_div(ceil_div(T, sms), 32) * 32, 65504);     // (counts are 16 bits)
     return ceil_div(T, per_block);
 }
 

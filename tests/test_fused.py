@@ -48,6 +48,11 @@ LINEAR = [
     (193, 1000, 1024, 128, True, "gelu", False, True, True),
     (500, 333, 2048, 128, False, None, False, False, False),
     (2048, 1026, 512, 128, True, "silu", True, False, True),
+    # a product of two halves without an activation; rows too long for shared memory
+    (4, 66, 256, 128, True, None, True, True, True),
+    (40, 130, 256, 64, False, None, True, False, False),
+    (1, 40, 131072, 128, True, None, False, False, True),
+    (3, 40, 262144, 256, True, None, False, True, False),
 ]
 
 
@@ -230,6 +235,19 @@ def test_linear_grouped(lib, c, gap):
     _check_grouped(y, X, w, G, b, rows, offsets, act, gated)
     y[gap:n_rows - gap] = NAN                 # everything else is as it was
     assert torch.isnan(buf).all()
+
+
+@pytest.mark.parametrize("counts", [[2, 0, 3], [40, 9, 0], [150, 200, 30]])
+@pytest.mark.parametrize("gather", [False, True])
+def test_linear_grouped_strided_rows(lib, counts, gather):
+    """X as columns of a wider tensor, in place and gathered (with and without the copy)."""
+    N, K, G = 130, 384, 128
+    w, X, b, rows, offsets, n_rows = _grouped(65, counts, N, K, G, True, "relu", False, True, gather, T=70)
+    wide = torch.full((X.shape[0], K + 24), NAN, dtype=torch.float16, device="cuda")
+    wide[:, 16:16 + K] = X
+    y = lib.linear_grouped(wide[:, 16:16 + K], *w, offsets, rows, G, True, bias=b, activation="relu")
+    _finish(lib)
+    _check_grouped(y, X, w, G, b, rows, offsets, "relu", False)
 
 
 @pytest.mark.parametrize("n_rows", [5, 40, 300])
