@@ -52,6 +52,12 @@ __device__ __forceinline__ void mbar_wait_or_abort(uint64_t* bar, uint32_t parit
     mbar_wait_or_abort(smem_u32(bar), parity, smem_u32(const_cast<const uint32_t*>(abort)));
 }
 
+// Wait until the stream's previous kernel has completed, then let the next one start.  In this order the
+// next kernel's early reads (weights, in the decode form and the GEMV) come after everything before this one.
+__device__ __forceinline__ void grid_dependency_pass() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // 32 TMEM lanes x 8 consecutive 32-bit columns (as tmem_ld16).
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

@@ -169,10 +169,9 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         mbar_fence_init();
         prefetch_tensormap(&tmap_q);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Grouped, the table decides which weights are read; dense, the weights stream before the previous
     // kernel has completed, and only X, the residual and Y wait for it (below).
-    if (a.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.offsets) grid_dependency_pass();
     DecSeg* segs = reinterpret_cast<DecSeg*>(smem + L.segs());
     if (warp == 1) {
         // this CTA's share of all row sets' units, as segments
@@ -393,7 +392,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     const int m0 = 2 * t, m1 = 2 * t + 1;
     int st = 0, b = 0;
     uint32_t ph = 0, rph = 0;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_dependency_pass();
     for (int i = 0; i < nseg; ++i) {
         const DecSeg sg = segs[i];
         // X of the segment: 16-byte chunks reordered within each k-step to [j][t] with the middle words

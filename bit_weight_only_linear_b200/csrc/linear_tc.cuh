@@ -240,8 +240,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         tmem_alloc(&misc[0], C::kTmemCols);
         tmem_relinquish();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_dependency_pass();
     if (warp == 0) {
         // the CTA's tile and the rows of X that it reads
         int4 t;
@@ -665,7 +664,7 @@ constexpr int kGatherThreads = 256;
 __global__ void __launch_bounds__(kGatherThreads)
 gather_rows_kernel(const uint16_t* __restrict__ X, int T, long long ldx, const int32_t* __restrict__ rows, int R,
                    const int32_t* __restrict__ offsets, int E, int K, uint16_t* __restrict__ out) {
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    sm100::grid_dependency_pass();
     const int lane = threadIdx.x & 31;
     const int begin = min(max(__ldg(offsets), 0), R), end = min(max(__ldg(offsets + E), 0), R);
     for (long long p = begin + (long long)blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5); p < end;

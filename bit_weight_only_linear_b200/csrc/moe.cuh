@@ -111,14 +111,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     __shared__ int base[kRouteMaxExperts + 1];
     __shared__ int warp_sums[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
         run[e] = 0;
 #pragma unroll
         for (int w = 0; w < kRouteWords; ++w) mask[w][e] = 0;
     }
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    sm100::grid_dependency_pass();
     const int t_begin = blockIdx.x * a.per_block;
     const int t_end = min(a.T, t_begin + a.per_block);
     for (int t0 = t_begin; t0 < t_end; t0 += kRoutePass) {
@@ -267,14 +266,13 @@ __global__ void __launch_bounds__(kRouteWalkThreads) route_walk_kernel(RouteArgs
     const int q = threadIdx.x & 3, tok = threadIdx.x >> 2;          // lane of the token, token of the pass
     const int word = tok >> 5;
     const uint32_t bit = 1u << (tok & 31);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e = threadIdx.x; e < a.E; e += kRouteWalkThreads) {
         run[e] = 0;
 #pragma unroll
         for (int w = 0; w < kRouteWords; ++w) mask[w][e] = 0;
     }
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    sm100::grid_dependency_pass();
     const int t_begin = blockIdx.x * a.per_block;
     const int t_end = min(a.T, t_begin + a.per_block);
     constexpr int kOwn = (KT + 3) / 4;                              // slots that a lane writes
@@ -424,7 +422,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_order_kernel(RouteArgs a)
     __shared__ int warp_sums[32];
     for (int e = threadIdx.x; e < a.E; e += kRouteThreads) total[e] = before[e] = 0;
     __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    sm100::grid_dependency_pass();
     // thread (part, expert): the counts of every parts-th block (integer sums: order-free)
     const int parts = max(1, kRouteThreads / a.E);
     const int e0 = threadIdx.x % a.E, part = threadIdx.x / a.E;
@@ -512,7 +510,7 @@ combine_kernel(const uint16_t* __restrict__ Y, int R, long long ldy, const float
     using Vec = typename HalfVec<V>::T;
     const size_t t = blockIdx.x;
     const int n = (blockIdx.y * kCombineThreads + threadIdx.x) * V;
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    sm100::grid_dependency_pass();
     if (n >= N) return;
     float acc[V] = {};
     constexpr int kAhead = 4;                        // rows in flight per thread
