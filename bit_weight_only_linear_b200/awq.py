@@ -407,15 +407,18 @@ def _activation(activation) -> int:
 def _weights(lead, qweight, scales, qzeros, K, group_size, zero_point, index):
     """(N, data pointers) of packed weights with the leading axes `lead` (() or (E,))."""
     shape = qweight.shape
-    if len(shape) != len(lead) + 2 or shape[-1] * 8 != K or shape[:-2] != lead:
+    if len(shape) != len(lead) + 2 or shape[-1] * 8 != K:
         raise ValueError(f"qweight has shape {tuple(shape)}, expected {[*lead, 'N', K // 8]}")
     if zero_point == (qzeros is None):
         raise ValueError("qzeros must be given with zero_point and left out without")
-    if group_size not in (32, 64, 128, 256) or K % group_size:
+    if group_size not in _GROUP_SIZES or K % group_size:
         raise ValueError(f"group_size {group_size} is not 32, 64, 128 or 256, or does not divide K = {K}")
     N, ng = shape[-2], K // group_size
     return (N, _flat(qweight, "qweight", index, shape, _W32), _flat(scales, "scales", index, (*lead, N, ng), _F16),
-            _flat(qzeros, "qzeros", index, (*lead, N, (ng + 7) // 8), _W32))
+            0 if qzeros is None else _flat(qzeros, "qzeros", index, (*lead, N, (ng + 7) // 8), _W32))
+
+
+_GROUP_SIZES = frozenset((32, 64, 128, 256))
 
 
 def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bias=None, activation=None,
@@ -432,13 +435,15 @@ def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bi
     if gated and N & 1:
         raise ValueError("a gated linear needs an even number of weight rows")
     n_out = N // 2 if gated else N
-    if out is None:
-        out = X.new_empty((M, n_out))
     px, ldx = _rows(X, "X", dev, M, K)
     pr, ldr = _rows(residual, "residual", dev, M, n_out)
-    py, ldy = _rows(out, "out", dev, M, n_out)
+    if out is None:
+        out = X.new_empty((M, n_out))
+        py, ldy = out.data_ptr(), n_out
+    else:
+        py, ldy = _rows(out, "out", dev, M, n_out)
     _linear_fused(dev, stream, px, M, ldx, pq, ps, pz, N, K, _config(group_size, zero_point),
-        _flat(bias, "bias", dev, (N,), _F16), act, 1 if gated else 0, pr, ldr, py, ldy)
+                  _flat(bias, "bias", dev, (N,), _F16), act, 1 if gated else 0, pr, ldr, py, ldy)
     return out
 
 
@@ -473,10 +478,12 @@ def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=12
         raise ValueError("a gated linear needs an even number of weight rows")
     n_out = N // 2 if gated else N
     R = T if rows is None else rows.shape[0]
+    px, ldx = _rows(X, "X", dev, T, K)
     if out is None:
         out = X.new_empty((R, n_out))
-    px, ldx = _rows(X, "X", dev, T, K)
-    py, ldy = _rows(out, "out", dev, R, n_out)
+        py, ldy = out.data_ptr(), n_out
+    else:
+        py, ldy = _rows(out, "out", dev, R, n_out)
     if workspace is None and R >= _GATHER_MIN_SHARE * E and rows is not None:
         need = (_lib or load_library()).awq_linear_grouped_workspace_bytes(R, E, K)
         if need:
@@ -511,20 +518,25 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
         raise ValueError(f"scoring {scoring!r} is not one of {sorted(SCORINGS)}")
     pl, ld = _rows(logits, "logits", dev, T, E, torch.float16 if half else torch.float32)
     if out is None:
-        experts, positions, rows = logits.new_empty((3, T, top_k), dtype=torch.int32).unbind()
+        ints = logits.new_empty((3, T, top_k), dtype=torch.int32)
+        experts, positions, rows = ints.unbind()
         out = MoeRoute(logits.new_empty((T, top_k), dtype=torch.float32), experts,
                        logits.new_empty(E + 1, dtype=torch.int32), rows.view(-1), positions)
-    weights, experts, offsets, rows, positions = out
-    slots = (T, top_k)
+        pe, step = ints.data_ptr(), 4 * T * top_k
+        pointers = out.weights.data_ptr(), pe, out.offsets.data_ptr(), pe + 2 * step, pe + step
+    else:
+        weights, experts, offsets, rows, positions = out
+        slots = (T, top_k)
+        pointers = (_flat(weights, "weights", dev, slots, _F32), _flat(experts, "experts", dev, slots, _I32),
+                    _flat(offsets, "offsets", dev, (E + 1,), _I32), _flat(rows, "rows", dev, (T * top_k,), _I32),
+                    _flat(positions, "positions", dev, slots, _I32))
     if workspace is None:
         need = _route_need(T, E, dev)
         if need:
             workspace = _scratch(logits, need, stream)
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _moe_route(dev, stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0,
-        _flat(weights, "weights", dev, slots, _F32), _flat(experts, "experts", dev, slots, _I32),
-        _flat(offsets, "offsets", dev, (E + 1,), _I32), _flat(rows, "rows", dev, (T * top_k,), _I32),
-        _flat(positions, "positions", dev, slots, _I32), ws, ws_bytes)
+    _moe_route(dev, stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0, *pointers, ws,
+               ws_bytes)
     return out
 
 
@@ -551,11 +563,13 @@ def moe_combine(Y, weights, positions, residual=None, out=None, stream=None) -> 
     if positions.dim() != 2:
         raise ValueError("positions must have 2 dimensions")
     T, k = slots = positions.shape
-    if out is None:
-        out = Y.new_empty((T, N))
     py, ldy = _rows(Y, "Y", dev, R, N)
     pr, ldr = _rows(residual, "residual", dev, T, N)
-    po, ldo = _rows(out, "out", dev, T, N)
+    if out is None:
+        out = Y.new_empty((T, N))
+        po, ldo = out.data_ptr(), N
+    else:
+        po, ldo = _rows(out, "out", dev, T, N)
     _moe_combine(dev, stream, py, R, ldy, _flat(weights, "weights", dev, slots, _F32),
         _flat(positions, "positions", dev, slots, _I32), T, k, N, pr, ldr, po, ldo)
     return out
