@@ -253,15 +253,19 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
                 if (g0 < ng) {
                     if (vec) {
                         fs[o] = __ldg(reinterpret_cast<const uint4*>(sp + g0));
+                    } else if ((ng & 1) == 0) {
+                        // rows of other lengths in words or halves, all loads in flight together (one after the
+                        // other they took longer than the stage: 34 experts x 2048 x 1408, G = 64: 39 us)
+                        const uint32_t* wp = reinterpret_cast<const uint32_t*>(sp + g0);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = g0 + 2 * i < ng ? __ldg(wp + i) : 0u;
+                        fs[o] = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
-                        unsigned long long w[2] = {0ull, 0ull};
-#pragma unroll 1
-                        for (int i = 0; i < 8 && g0 + i < ng; ++i) {
-                            const unsigned long long v = (unsigned long long)__ldg(sp + g0 + i) << (16 * (i & 3));
-                            if (i < 4) w[0] |= v;
-                            else w[1] |= v;
-                        }
-                        fs[o] = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+                        uint32_t h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[i] = g0 + i < ng ? __ldg(sp + g0 + i) : 0u;
+                        fs[o] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
                     }
                     if (zp) fz[o] = __ldg(a.qzeros + wr * nzw + (g0 >> 3));
                 }

@@ -67,6 +67,35 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One code pair of a word as fp16 1024 + q: (word & mask) | 0x6400 in both halves.  As one lop3: written in C it
+// becomes two instructions, since each takes one immediate, and with 16 rows a tile the integer pipe's 9 per word
+// instead of 5 were what the conversion waited for (96 tokens, 6 of 64 experts, 2816 x 2048: 71 -> 65 us).
+__device__ __forceinline__ uint32_t code_pair(uint32_t word, uint32_t mask) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(word), "r"(mask), "r"(0x64006400u));
+    return r;
+}
+
+// (q - z) * s for the 8 codes of a word, as 4 fp16 pairs in k order; the two codes of a pair sit at the same nibble
+// of the word's halves.  q - z is exact, the product is rounded once.
+__device__ __forceinline__ uint4 dequant_codes(uint32_t word, uint32_t zmagic, uint32_t zneg16, uint32_t s2) {
+    uint32_t a = code_pair(word, 0x000F000Fu);             // 1024 + q
+    uint32_t b = code_pair(word, 0x00F000F0u);             // 1024 + 16 q
+    uint32_t c = code_pair(word >> 8, 0x000F000Fu);
+    uint32_t d = code_pair(word >> 8, 0x00F000F0u);
+    asm("sub.rn.f16x2 %0, %0, %4;\n\t"                     // less 1024 + z
+        "sub.rn.f16x2 %2, %2, %4;\n\t"
+        "fma.rn.f16x2 %1, %1, %5, %6;\n\t"                 // a sixteenth, less 64 + z
+        "fma.rn.f16x2 %3, %3, %5, %6;\n\t"
+        "mul.rn.f16x2 %0, %0, %7;\n\t"
+        "mul.rn.f16x2 %1, %1, %7;\n\t"
+        "mul.rn.f16x2 %2, %2, %7;\n\t"
+        "mul.rn.f16x2 %3, %3, %7;"
+        : "+r"(a), "+r"(b), "+r"(c), "+r"(d)
+        : "r"(zmagic), "r"(0x2C002C00u), "r"(zneg16), "r"(s2));
+    return make_uint4(a, b, c, d);
+}
+
 // 16 bytes global -> shared, or zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
@@ -487,7 +516,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const uint32_t word = w == 0 ? packed.x : (w == 1 ? packed.y : (w == 2 ? packed.z : packed.w));
-                        const uint4 d = dequant_word(word, zmagic, zneg16, s2);
+                        const uint4 d = dequant_codes(word, zmagic, zneg16, s2);
                         v[4 * w] = d.x, v[4 * w + 1] = d.y, v[4 * w + 2] = d.z, v[4 * w + 3] = d.w;
                     }
                     // the codes are converted before the wait for the MMAs that read this buffer
