@@ -17,8 +17,8 @@
 //     the K of each half, so half as many partial sums meet per row.  With few, 32 rows (RS = 1) share out
 //     more evenly.
 //   * Warps: a producer (3-D TMA, 32 KB stages of 32 rows x 2048 codes), two converters (scales and
-//     zeros -> fp32 pairs per stage), 16 consumers (128 codes of a stage each), a reducer (the
-//     consumers' partial sums in a fixed order, then the epilogue).
+//     zeros -> fp32 pairs per stage), 16 consumers (128 codes of a stage each), a reducer for each 32
+//     rows of the unit (the consumers' partial sums in a fixed order, then the epilogue).
 // Bound: HBM where CTAs get many units (8 tokens, 2 of 8 experts, 28672 x 4096: 80 us = 5.5 TB/s, 0.84 of the
 // measured copy rate); for one dense matrix the start and end of a launch, about 4 us, and the uneven last
 // unit (1 row x 28672 x 4096, gated: 15.6 us = 3.9 TB/s; 4096 x 4096: 4.8 us).
@@ -37,8 +37,8 @@ namespace awq {
 
 constexpr int kDecConsumers = 16;
 constexpr int kDecConverters = 2;
-constexpr int kDecReducer = 1 + kDecConverters, kDecConsumer0 = kDecReducer + 1;   // first warps of the roles
-constexpr int kDecThreads = (kDecConsumer0 + kDecConsumers) * 32;
+constexpr int kDecReducer0 = 1 + kDecConverters;  // first reducer's warp; RS reducers, then the consumers
+constexpr int dec_threads(int RS) { return (kDecReducer0 + RS + kDecConsumers) * 32; }
 constexpr int kDecRows = 32;                     // weight rows of a consumer: two MMA row tiles
 constexpr int kDecStageBytes = 32 * 1024;        // 32 RS rows x 2048 / RS codes
 constexpr int kDecMaxRows = 8;                   // rows of X at a time (MMA N)
@@ -136,7 +136,7 @@ struct DecIter {
 };
 
 template <int G, int RS>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__(dec_threads(RS), 1)
 linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a) {
     using namespace sm100;
     constexpr int WT = gemv_words_per_thread(G);
@@ -145,6 +145,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     constexpr int KC = 2048 / RS;                          // codes per row and stage
     constexpr int GPC = KC / G;                            // groups per row and stage
     constexpr int KS = kDecConsumers / RS;                 // consumers that share the K of 32 rows
+    constexpr int kConsumer0 = kDecReducer0 + RS;          // first consumer's warp
     constexpr int kSub = kDecStageBytes / RS;              // their part of a stage
     extern __shared__ __align__(128) uint8_t smem[];
     const DecSmem L(a.mc, a.K, G, a.S, RS);
@@ -163,7 +164,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&rfull[i], kDecConsumers);
-            mbar_init(&rempty[i], 1);
+            mbar_init(&rempty[i], RS);
         }
         *abort = 0;
         mbar_fence_init();
@@ -226,7 +227,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         for (int j = issued - 1; j >= 0 && j >= issued - S; --j) mbar_wait(&full[j % S], (j / S) & 1);
         return;
     }
-    if (warp < kDecReducer) {
+    if (warp < kDecReducer0) {
         // ---------------- converters: lane = row of each part of the unit.  Each takes every second stage and holds
         // the scales and zero words of the next kDepth of them in registers (a stage's loads take longer
         // than the stage streams) ----------------
@@ -312,9 +313,12 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
         }
         return;
     }
-    if (warp == kDecReducer) {
-        // ---------------- reducer: the consumers' sums in order, then the epilogue.  Lane = (row of X,
-        // four weight rows), two rows of X a lane; 16-byte reads, all independent ----------------
+    if (warp < kConsumer0) {
+        // ---------------- reducers: the consumers' sums in order, then the epilogue.  Lane = (row of X,
+        // four weight rows); 16-byte reads, all independent.  A warp for each 32 rows of the unit: with one for
+        // both, the chain of reads, activation and stores took longer than the weights where K is short
+        // (3 rows each of 64 experts, 2816 x 2048, gated: 51 -> 40 us; with three or more the consumers have too
+        // few registers: 43) ----------------
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const Epilogue& ep = a.ep;
         const int quad = lane & 7;
@@ -327,47 +331,45 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
                 mbar_wait_or_abort(&rfull[b], ph, abort);
                 __syncwarp();
                 const uint32_t slot = sbase + (uint32_t)(L.part() + b * L.part_stride() + quad * 16);
+                const int p = warp - kDecReducer0;
+                const int row = quad < 4 ? tile0(n, p) + quad * 4 : tile1(n, p) + quad * 4 - 16;
                 const int lim = ep.gated && quad < 4 ? F : a.N;
+                float bv[4] = {};
+                if (bias) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (row + i < lim) bv[i] = h2f(__ldg(bias + row + i));
+                }
                 // (not unrolled, here and in the other rare paths: the roles share the instruction cache, and
-                // what they fetch anew for every unit shows: 61 -> 55 us on 64 experts of 3 rows)
+                // what they fetch anew for every unit shows: 61 -> 55 us on 64 experts of 3 rows; 8-byte stores
+                // with a second path for odd strides gain nothing)
 #pragma unroll 1
-                for (int p = 0; p < RS; ++p) {
-                    const int row = quad < 4 ? tile0(n, p) + quad * 4 : tile1(n, p) + quad * 4 - 16;
-                    float bv[4] = {};
-                    if (bias) {
+                for (int it = 0; it * 4 < sg.nr; ++it) {
+                    const int m = it * 4 + (lane >> 3), mm = min(m, sg.nr - 1);
+                    const bool store = m < sg.nr && (!ep.gated || quad < 4);
+                    float y[4] = {}, res[4] = {}, other[4];
+                    if (ep.residual && store) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (row + i < lim) bv[i] = h2f(__ldg(bias + row + i));
+                            if (row + i < lim) res[i] = h2f(ep.residual[(size_t)(sg.r0 + m) * ep.ldr + row + i]);
                     }
-#pragma unroll 1
-                    for (int it = 0; it * 4 < sg.nr; ++it) {
-                        const int m = it * 4 + (lane >> 3), mm = min(m, sg.nr - 1);
-                        const bool store = m < sg.nr && (!ep.gated || quad < 4);
-                        float y[4] = {}, res[4] = {};
-                        if (ep.residual && store) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (row + i < lim) res[i] = h2f(ep.residual[(size_t)(sg.r0 + m) * ep.ldr + row + i]);
-                        }
+                    for (int w = 0; w < KS; ++w) {
+                        const uint4 v = lds128(slot + (uint32_t)(((p * KS + w) * a.mc + mm) * kDecPartPitch * 4));
+                        y[0] += __uint_as_float(v.x), y[1] += __uint_as_float(v.y);
+                        y[2] += __uint_as_float(v.z), y[3] += __uint_as_float(v.w);
+                    }
 #pragma unroll
-                        for (int w = 0; w < KS; ++w) {
-                            const uint4 v = lds128(slot + (uint32_t)(((p * KS + w) * a.mc + mm) * kDecPartPitch * 4));
-                            y[0] += __uint_as_float(v.x), y[1] += __uint_as_float(v.y);
-                            y[2] += __uint_as_float(v.z), y[3] += __uint_as_float(v.w);
-                        }
-                        float other[4];
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] += bv[i];
+                        other[i] = __shfl_down_sync(0xffffffffu, y[i], 4);
+                    }
+                    apply_act(y, ep.act);
+                    uint16_t* yp = ep.Y + (size_t)(sg.r0 + m) * ep.ldy + row;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            y[i] += bv[i];
-                            other[i] = __shfl_down_sync(0xffffffffu, y[i], 4);
-                        }
-                        apply_act(y, ep.act);
-                        uint16_t* yp = ep.Y + (size_t)(sg.r0 + m) * ep.ldy + row;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (ep.gated) y[i] *= other[i];
-                            if (store && row + i < lim) yp[i] = f2h_rn(y[i] + res[i]);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        if (ep.gated) y[i] *= other[i];
+                        if (store && row + i < lim) yp[i] = f2h_rn(y[i] + res[i]);
                     }
                 }
                 __syncwarp();
@@ -382,7 +384,7 @@ linear_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const DecArgs a
     constexpr int kCons = kDecConsumers * 32;
     constexpr int R = G >= kStepCodes ? G / kStepCodes : 1;     // k-steps per group
     constexpr int TPS = 4 * WT;                                  // 16-byte chunks per k-step
-    const int cw = warp - kDecConsumer0, ct = threadIdx.x - kDecConsumer0 * 32;
+    const int cw = warp - kConsumer0, ct = threadIdx.x - kConsumer0 * 32;
     const int g = lane >> 2, t = lane & 3;
     const int pitch = L.x_pitch();
     uint8_t* xs = smem + L.x();
@@ -553,7 +555,7 @@ inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d,
     const long long grid = std::min<long long>(d.sms, sets * a.units);
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)grid);
-    lc.blockDim = dim3(kDecThreads);
+    lc.blockDim = dim3((unsigned)dec_threads(RS));
     lc.dynamicSmemBytes = DecSmem(mc, l.K, l.G, S, RS).bytes();
     lc.stream = st;
     cudaLaunchAttribute attr[1];
@@ -563,6 +565,25 @@ inline awq_status launch_linear_decode(const LinearArgs& l, const DeviceInfo& d,
     lc.numAttrs = 1;
     void* args[] = {&tq, &a};
     return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+// Whether 16-row tensor-core tiles, two CTAs to an SM, are the faster form for experts whose units are 64 rows.
+// Modelled times (us): a decode stage of 64 rows x 1024 codes takes 0.87 with G = 128 (1.17 where rows of an odd
+// number of scales are read by halves), 1.13 with 64 and 1.75 with 32, a unit at least 1.2, and 8 are spent around
+// them; a tile's 64 codes take 0.66 to 0.78 while two tiles share an SM, and 9 around them.  Measured, decode against
+// tiles, 64 experts of 2048 channels: 3 rows each, G = 128, K = 512 23 / 19, 2048 32 / 44, 4096 53 / 80; G = 64 25 / 19,
+// 37 / 46, 68 / 87; G = 32 29 / 20, 53 / 52, 102 / 96.  6 rows: G = 128 39 / 45, G = 64 48 / 48, G = 32 70 / 55.
+inline bool experts_prefer_tiles(const LinearArgs& l, int sms, int mc) {
+    const int active = std::min(l.R, l.E);
+    const long long tiles = (long long)active * (l.ep.gated ? ceil_div(l.N / 2, 128) : ceil_div(l.N, kTcRows));
+    if (2 * tiles < 3LL * sms) return false;               // (fewer tiles do not fill the SMs twice: another form)
+    // experts of 8 rows on average take 1.5 sets each, of 4 rows one
+    const double sets = active + std::max(0.0, (double)l.R / mc - 0.5 * active);
+    const double units = sets * (l.ep.gated ? ceil_div(l.N / 2, 32) : ceil_div(l.N, 64));
+    const double stage = l.G == 32 ? 1.75 : (l.G == 64 ? 1.13 : ((l.K / l.G) & 1 ? 1.17 : 0.87));
+    const double decode = 8.0 + units / sms * std::max(1.2, stage * ceil_div(l.K, 1024));
+    const double codes64 = l.G == 32 ? 0.78 : (l.G == 64 ? 0.70 : 0.66);
+    return 9.0 + tiles / (2.0 * sms) * ceil_div(l.K, kGemmKB) * codes64 < decode;
 }
 
 // Which form takes a call.  The decode form takes up to 8 rows a matrix and whole 128-code blocks; above
@@ -584,6 +605,7 @@ inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaSt
                    (share <= kDecMaxRows || S >= 3);
         // a CTA's list of segments must hold the row sets that its units may reach
         const long long sets = !fits ? 0 : (l.offsets ? (long long)l.R / mc + std::min(l.R, l.E) : ceil_div(l.R, mc));
+        if (fits && l.offsets && RS == 2 && experts_prefer_tiles(l, d.sms, mc)) fits = false;
         if (fits && sets <= (long long)(kDecMaxSegs - 2) * d.sms && sets * ceil_div(l.N, 32) < 0x7fffffffLL)
             return launch_linear_decode(l, d, RS, mc, S, st);
     }

@@ -24,8 +24,8 @@
 // Bound: the tensor cores from about 150 rows on (2048 rows x 57344 x 8192, gated: 1.33 ms = 1450 TFLOP/s,
 // 0.87 of the measured burst rate, above the sustained one); the round trip between conversion and MMA,
 // 0.3 us per 64 codes of 256 rows, below (61 rows x 4096 x 14336: 24 us, of which 8 are the start and the
-// exchange of the splits); with 16 rows a tile the issue of the conversion (96 tokens, 6 of 64 experts, 2816 x
-// 2048: 71 us = 2.8 TB/s).
+// exchange of the splits); with tiles of few rows the issue of the conversion (96 tokens, 6 of 64 experts,
+// 2816 x 2048: 62 us = 3.2 TB/s).
 // Each dequantised weight is rounded once to fp16, as in awq_linear_gemm, whose range flag it
 // raises too.  Every wait is bounded: on time-out the kernel raises the device error word, drains
 // what it issued, frees TMEM and returns.
@@ -856,11 +856,14 @@ inline awq_status launch_linear_tc(const LinearArgs& l, int sms, cudaStream_t st
     const int n_tiles = l.ep.gated ? ceil_div(l.N / 2, 128) : ceil_div(l.N, kTcRows);
     const int num_kb = ceil_div(l.K, kGemmKB);
     // Few rows and many tiles: two CTAs on an SM hide each other's start and end (64 experts of 9 rows, 2816 x
-    // 2048: 72 us at 16 rows a tile against 101 with one CTA; with fewer tiles than SMs it is the reverse,
-    // 16 tiles of 61 rows x 14336 in 6 parts: 25 us against 28)
+    // 2048: 62 us at 32 rows a tile against 92 with one CTA; with fewer tiles than SMs it is the reverse,
+    // 16 tiles of 61 rows x 14336 in 6 parts: 24 us against 28).  A tile holds 2.2 times the experts' average,
+    // since a second tile reads an expert's weights again (the same experts at tiles of 16 / 32 / 64 rows, 6 rows
+    // each: 61 / 62 / 65 us, 9: 65 / 62 / 65, 12: 69 / 63 / 66, 16: 78 / 67 / 67, 19: 87 / 71 / 67).
     if (m <= 64 && 2LL * active * n_tiles >= 3LL * sms) {
-        if (m <= 16) return launch_tc_bn<16>(l, 1, st);
-        if (m <= 32) return launch_tc_bn<32>(l, 1, st);
+        const long long hold = l.offsets ? ((long long)l.R * 11 + active * 5 - 1) / (active * 5) : l.R;
+        if (hold <= 16) return launch_tc_bn<16>(l, 1, st);
+        if (hold <= 32) return launch_tc_bn<32>(l, 1, st);
         return launch_tc_bn<64>(l, 1, st);
     }
     LinearArgs in_place = l;

@@ -245,9 +245,9 @@ enum {
  * rows in elements; ldx a multiple of 8 (X 16-byte aligned as ever), while bias, residual
  * and Y need only their element's alignment.  N need not be a multiple of anything.
  * M <= 2^30, N <= 2^31 - 512.
- * Needs no workspace.  Range: a batch on the tensor-core tiles (always above 16 rows) rounds each
- * dequantised weight once to fp16 and reports AWQ_ERR_RANGE as awq_linear_gemm does; calls of few rows
- * multiply codes and scales exactly and have no such limit.
+ * Needs no workspace.  Range: a batch on the tensor-core tiles (always above 16 rows; grouped, also few
+ * rows of each of many experts) rounds each dequantised weight once to fp16 and reports AWQ_ERR_RANGE as
+ * awq_linear_gemm does; other calls multiply codes and scales exactly and have no such limit.
  * Ordering: as awq_linear_gemv, a call may read the weights before the previous kernel on `stream` has
  * completed, so that kernel must not write them (the quantisers end with an ordering kernel of theirs).
  */
