@@ -237,6 +237,47 @@ def test_linear_grouped(lib, c, gap):
     assert torch.isnan(buf).all()
 
 
+MANY_EXPERTS = [
+    # rows of an expert below, K, G, zero_point, activation, gated, bias: 64-row units (2048 / 1024 codes a row) or
+    # 16-row tiles, by length; K / G odd, even and a multiple of 8
+    (4, 512, 128, True, None, False, True),
+    (4, 896, 128, True, "silu", True, False),
+    (4, 896, 32, True, "relu", False, True),
+    (4, 1408, 128, True, "silu", True, True),
+    (4, 1408, 64, False, None, False, False),
+    (11, 2048, 128, True, "gelu", True, True),
+    (11, 2048, 64, True, None, False, True),
+    (11, 1152, 32, True, "silu", True, False),
+    (21, 640, 128, True, "silu", True, True),
+    (41, 640, 64, True, None, False, True),
+]
+
+
+@pytest.mark.parametrize("c", MANY_EXPERTS, ids=lambda c: "-".join(map(str, c)))
+def test_linear_grouped_many_experts(lib, c):
+    """Uneven shares of 64 experts: none, one, above 4 and above 8 rows (a second set), above a tile's."""
+    below, K, G, zp, act, gated, bias = c
+    counts = [5 * e % below for e in range(64)]
+    w, X, b, rows, offsets, n_rows = _grouped(66, counts, 770, K, G, zp, act, gated, bias, True, gap=2)
+    y = lib.linear_grouped(X, *w, offsets, rows, G, zp, bias=b, activation=act, gated=gated,
+                           out=torch.full((n_rows, 385 if gated else 770), NAN, dtype=torch.float16, device="cuda"))
+    _finish(lib)
+    _check_grouped(y, X, w, G, b, rows, offsets, act, gated)
+    assert torch.isnan(y[:2]).all() and torch.isnan(y[-2:]).all()
+
+
+@pytest.mark.parametrize("M", [1, 5, 8, 14])
+@pytest.mark.parametrize("K,G", [(640, 128), (640, 64), (896, 32), (1408, 128), (11008, 128)])
+def test_linear_fused_lengths_of_scale_rows(lib, M, K, G):
+    """Rows of 5, 10, 28, 11 and 86 scales: read by halves and by words."""
+    w = R.packed(67, 130, K, G, True)
+    X = R.activations(68, M, K)
+    y = lib.linear_fused(X, *w, G, True)
+    _finish(lib)
+    ref, bound = R.linear64(X, w, G, None, None, False, None)
+    R.assert_close(y, ref, bound, False)
+
+
 @pytest.mark.parametrize("counts", [[2, 0, 3], [40, 9, 0], [150, 200, 30]])
 @pytest.mark.parametrize("gather", [False, True])
 def test_linear_grouped_strided_rows(lib, counts, gather):
