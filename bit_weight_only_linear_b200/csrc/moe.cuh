@@ -12,7 +12,7 @@
 //     order).  Blocks take contiguous ranges of tokens and publish their counts; the second kernel
 //     adds the counts of the blocks before its own.  One block needs no second kernel.
 // Bound: a launch's latency for decode (8 tokens, 8 experts: 3.7 us); for a long prefill the latency of the
-// walks and of the second launch (16384 tokens, top 8 of 128, fp16: 24 us).
+// walks and of the second launch (16384 tokens, top 8 of 128, fp16: 15 us).
 //
 // Combination.  out[t] = residual[t] + sum_j w[t][j] Y[positions[t][j]], fp32 sums in slot order,
 // one rounding: bound by reading the T top_k rows once (8192 tokens x 8 x 4096: 103 us = 6.46 TB/s, 0.99 of the
@@ -32,9 +32,7 @@ constexpr int kRouteMaxTopK = 32;
 constexpr int kRouteThreads = 1024;     // 32 warps
 constexpr int kRouteWords = 4;          // tokens of a warp in a pass; mask words of an expert
 constexpr int kRoutePass = 32 * kRouteWords;
-// Tokens that one block takes alone in a single launch, and from which four lanes take a token.
-constexpr int kRouteSingle = 32;
-constexpr int kRouteWalkMin = 12288;
+constexpr int kRouteSingle = 32;        // tokens that one block takes alone in a single launch
 
 struct RouteArgs {
     const void* logits;
@@ -247,7 +245,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     for (int p = base[a.E] + threadIdx.x; p < slots; p += kRouteThreads) a.rows[p] = -1;
 }
 
-// Four lanes per token, for many tokens and top_k <= KT (2, 4 or 8): each lane walks a quarter of the row
+// Four lanes per token, for top_k <= KT (2, 4 or 8): each lane walks a quarter of the row
 // and keeps its KT largest in registers, one compare and a shift per slot; two bitonic merges make the
 // token's list.  8 tokens share each instruction (about 200 a token at 128 experts and KT = 8, against 610
 // for the warp form, whose reductions serve one token); a single lane per token needs no merge, but 16384
@@ -470,6 +468,15 @@ inline size_t route_workspace_bytes(int T, int E, int sms) {
     return blocks > 1 ? align256((size_t)blocks * E * 2) : 0;
 }
 
+// Whether four lanes take a token instead of a warp (several blocks, top_k <= 8).  Measured, warp / four lanes, us:
+//   top 2 of 8:   256 tokens 5.9 / 5.2, 4096 6.3 / 5.4, 16384 11.1 / 5.6;    top 4 of 32: 256 5.9 / 5.9, 16384 12.9 / 7.3
+//   top 4 of 64:  256 6.3 / 6.8, 4096 7.7 / 7.8, 8192 9.8 / 8.0;  top 2 of 128: 256 7.0 / 7.0, 4096 8.3 / 8.2, 8192 11.0 / 8.4
+//   top 8 of 128: 256 7.7 / 12.6, 8192 12.7 / 14.4, 10240 16.8 / 15.4, 16384 19.4 / 14.9
+inline bool route_by_walk(const RouteArgs& a) {
+    if (a.blocks == 1 || a.k > 8) return false;
+    return a.E * a.k <= 128 || a.T >= (a.k <= 4 ? 6144 : 9216);
+}
+
 inline awq_status launch_route(RouteArgs a, cudaStream_t st) {
     const void* fn = a.E <= 32    ? (const void*)route_kernel<1>
                      : a.E <= 64  ? (const void*)route_kernel<2>
@@ -479,7 +486,7 @@ inline awq_status launch_route(RouteArgs a, cudaStream_t st) {
                                   : (const void*)route_kernel<32>;
     void* args[] = {&a};
     int threads = kRouteThreads;
-    if (a.blocks > 1 && a.T >= kRouteWalkMin && a.k <= 8) {
+    if (route_by_walk(a)) {
         fn = a.k <= 2   ? (const void*)route_walk_kernel<2>
              : a.k <= 4 ? (const void*)route_walk_kernel<4>
                         : (const void*)route_walk_kernel<8>;

@@ -374,7 +374,8 @@ def _check_route(r, logits, k, scoring, renorm):
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 7, 7), (31, 33, 4), (32, 64, 6), (33, 128, 8), (100, 5, 1),
                                    (256, 16, 2), (257, 60, 4), (1000, 200, 10), (700, 257, 32), (300, 1024, 32),
-                                   (5000, 8, 2), (13000, 40, 7), (12300, 130, 3), (12288, 9, 2)])
+                                   (5000, 8, 2), (13000, 40, 7), (12300, 130, 3), (12288, 9, 2), (9216, 64, 8), (9215, 64, 8),
+                                   (6144, 72, 4), (6143, 72, 4), (33, 8, 2), (161, 32, 4)])
 @pytest.mark.parametrize("half", [False, True])
 @pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 def test_moe_route(lib, T, E, k, half, scoring, renorm):
@@ -402,6 +403,23 @@ def test_moe_route_special_logits(lib, dtype, scoring, renorm):
     r = lib.moe_route(x.cuda(), 3, scoring=scoring, renormalize=renorm)
     torch.cuda.synchronize()
     _check_route(r, x, 3, scoring, renorm)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E", [(104, 5), (104, 70), (6500, 70)])
+def test_moe_route_special_logits_of_many_tokens(lib, dtype, scoring, T, E):
+    """The same rows where tokens are shared out to blocks, by warps and by four lanes."""
+    low, inf = torch.finfo(dtype).min, math.inf
+    rows = [[0, 0, 0, 0, 0], [-0.0, 0.0, -0.0, 1, 1], [low] * 5, [low, low, 3, low, low], [-inf] * 5,
+            [-inf, 2, -inf, -inf, -inf], [inf, 1, inf, 0, 0], [inf] * 5, [NAN, 1, NAN, 2, NAN], [NAN] * 5,
+            [-inf, low, inf, NAN, 0], [-60, -61, -62, -80, -90], [60, 61, 62, 80, 90]]
+    x = torch.full((T, E), -inf, dtype=dtype)
+    at = torch.randperm(E, generator=torch.Generator().manual_seed(E))[:5]
+    x[:, at] = torch.tensor(rows, dtype=dtype).repeat(T // len(rows) + 1, 1)[:T]
+    r = lib.moe_route(x.cuda(), 3, scoring=scoring, renormalize=True)
+    torch.cuda.synchronize()
+    _check_route(r, x, 3, scoring, True)
 
 
 def test_moe_route_strided_logits_and_given_outputs(lib):
