@@ -451,6 +451,15 @@ _I32 = (torch.int32,)
 _GATHER_MIN_SHARE = 64   # rows per expert below which a grouped call asks for no workspace
 
 
+def _workspace(t: Optional[torch.Tensor], index: int):
+    """(data pointer, bytes) of a workspace of any type."""
+    if t is None:
+        return 0, 0
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _scratch(like: torch.Tensor, need: int, stream) -> torch.Tensor:
     """Workspace of one call, freed on its return: not to be reused before `stream` has passed it."""
     ws = like.new_empty(need, dtype=torch.uint8)
@@ -488,7 +497,7 @@ def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=12
         need = (_lib or load_library()).awq_linear_grouped_workspace_bytes(R, E, K)
         if need:
             workspace = _scratch(X, need, stream)
-    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, ws_bytes = _workspace(workspace, dev)
     _linear_grouped(dev, stream, px, T, ldx, _flat(rows, "rows", dev, (R,), _I32), R,
         _flat(offsets, "offsets", dev, (E + 1,), _I32), E, pq, ps, pz, N, K, _config(group_size, zero_point),
         _flat(bias, "bias", dev, (E, N), _F16), act, 1 if gated else 0, py, ldy, ws, ws_bytes)
@@ -514,6 +523,8 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
     T, E = logits.shape
     half = logits.dtype is torch.float16
     score = SCORINGS.get(scoring)
+    if not 1 <= top_k <= E:                  # before tensors of that size are made
+        raise AWQError("awq_moe_route", AWQ_ERR_INVALID_ARG)
     if score is None:
         raise ValueError(f"scoring {scoring!r} is not one of {sorted(SCORINGS)}")
     pl, ld = _rows(logits, "logits", dev, T, E, torch.float16 if half else torch.float32)
@@ -534,7 +545,7 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
         need = _route_need(T, E, dev)
         if need:
             workspace = _scratch(logits, need, stream)
-    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, ws_bytes = _workspace(workspace, dev)
     _moe_route(dev, stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0, *pointers, ws,
                ws_bytes)
     return out

@@ -266,6 +266,19 @@ def test_linear_grouped_many_experts(lib, c):
     assert torch.isnan(y[:2]).all() and torch.isnan(y[-2:]).all()
 
 
+@pytest.mark.parametrize("M", [1, 4, 6, 8, 13])
+@pytest.mark.parametrize("N,K,G,act,gated", [(38003, 256, 128, "relu", False), (75842, 1152, 64, "silu", True),
+                                             (38002, 1408, 32, None, False)])
+def test_linear_fused_many_rows_of_weights(lib, M, N, K, G, act, gated):
+    """64-row units with bias and residual, ragged in rows and in codes."""
+    c = (M, N, K, G, True, act, gated, True, True)
+    w, X, b, r = _case(c, 69)
+    y = lib.linear_fused(X, *w, G, True, bias=b, activation=act, gated=gated, residual=r)
+    _finish(lib)
+    ref, bound = R.linear64(X, w, G, b, act, gated, r)
+    R.assert_close(y, ref, bound, gated)
+
+
 @pytest.mark.parametrize("M", [1, 5, 8, 14])
 @pytest.mark.parametrize("K,G", [(640, 128), (640, 64), (896, 32), (1408, 128), (11008, 128)])
 def test_linear_fused_lengths_of_scale_rows(lib, M, K, G):

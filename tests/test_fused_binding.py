@@ -80,3 +80,18 @@ def test_route_and_combine_refusals(lib):
     with pytest.raises(lib.AWQError) as e:
         lib.moe_route(_t(1000, 8, dtype=torch.float32), 2, workspace=_t(16, dtype=torch.uint8))
     assert e.value.status == 3
+
+
+def test_workspaces_refused(lib):
+    """A workspace elsewhere than on the device, or in pieces; a top_k that no tensor could hold."""
+    w = R.packed(3, 64, 256, 64, True, lead=(2,))
+    X, o = _t(4, 256), _t(3, dtype=torch.int32)
+    l = _t(1000, 8, dtype=torch.float32)
+    for ws in (torch.zeros(1 << 16, dtype=torch.uint8), _t(1 << 16, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError):
+            lib.linear_grouped(X, *w, o, _t(4, dtype=torch.int32), 64, True, workspace=ws)
+        with pytest.raises(ValueError):
+            lib.moe_route(l, 2, workspace=ws)
+    for k in (-1, 1 << 40):
+        with pytest.raises(lib.AWQError):
+            lib.moe_route(l, k)
