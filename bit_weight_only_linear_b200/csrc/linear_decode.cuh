@@ -588,9 +588,10 @@ inline bool experts_prefer_tiles(const LinearArgs& l, int sms, int mc) {
 
 // Which form takes a call.  The decode form takes up to 8 rows a matrix and whole 128-code blocks; above
 // that the tensor-core tiles win.  A dense batch may also take two passes over the weights, which pays while
-// the second comes from L2 and X leaves room for a ring: 16 rows x 4096, 28672 channels 26 us against 29 for
-// the tiles, 4096 channels 8.7 against 10.1; 8 rows x 14336 20 against 22.  It does not where weights are
-// many (3 rows x 28672, 8192 channels: 61 against 48) or X is wide (16 rows x 14336: 32 against 21).
+// the second comes from L2 and X leaves room for a ring: 16 rows x 4096, 28672 channels 26 us against 27 for
+// the tiles, 4096 channels 8.6 against 9.8; 6 rows x 14336 17.4 against 19.8 (8 rows: 20.6 against 19.9).  It does
+// not where weights are many (3 rows x 28672, 8192 channels: 61 against 43) or X is wide (16 rows x 14336: 33
+// against 20).
 inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaStream_t st) {
     const int share = l.offsets ? ceil_div(l.R, std::min(l.R, l.E)) : l.R;
     // 64-row units where every CTA gets many, however the units fall (and a stage has 8 groups per row)

@@ -834,7 +834,8 @@ int tc_active_clusters(int splits) {
 }
 
 // Modelled time (us) of `tiles` tiles of `rows` rows of X with the K in `splits` parts, from measured
-// slopes: a k-block of 256 weight rows takes 0.30 us, or 3.5 ns per row of X (0.38 and 3.0 in the 192-row form); a
+// slopes: a k-block of 256 weight rows takes 0.30 us, or 3.5 ns per row of X (0.38 and 3.0 in the 192-row form;
+// 24 rows measure 0.31, 61 0.37, 96 0.45, 192 0.67, with the HBM's share where all SMs stream); a
 // tile 4 us (6) around them, and 7 (12) for the exchange of a split's partial sums.  A last partial wave
 // costs half of one on average.
 template <int BN>
