@@ -529,12 +529,13 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
         raise ValueError(f"scoring {scoring!r} is not one of {sorted(SCORINGS)}")
     pl, ld = _rows(logits, "logits", dev, T, E, torch.float16 if half else torch.float32)
     if out is None:
-        ints = logits.new_empty((3, T, top_k), dtype=torch.int32)
-        experts, positions, rows = ints.unbind()
-        out = MoeRoute(logits.new_empty((T, top_k), dtype=torch.float32), experts,
-                       logits.new_empty(E + 1, dtype=torch.int32), rows.view(-1), positions)
-        pe, step = ints.data_ptr(), 4 * T * top_k
-        pointers = out.weights.data_ptr(), pe, out.offsets.data_ptr(), pe + 2 * step, pe + step
+        slots = T * top_k                    # one allocation for the four of that size: most of this call's time
+        made = logits.new_empty_strided((4, T, top_k), (slots, top_k, 1), dtype=torch.int32)
+        offsets = logits.new_empty_strided((E + 1,), (1,), dtype=torch.int32)
+        weights, experts, positions, rows = made.unbind()
+        out = MoeRoute(weights.view(torch.float32), experts, offsets, rows.flatten(), positions)
+        p, step = made.data_ptr(), 4 * slots
+        pointers = p, p + step, offsets.data_ptr(), p + 3 * step, p + 2 * step
     else:
         weights, experts, offsets, rows, positions = out
         slots = (T, top_k)
