@@ -267,6 +267,7 @@ awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uin
  * values at capture.  Entries beyond the limits never read or write out of bounds: offsets
  * are clamped to 0 .. R, and a row number outside 0 .. T-1 counts as a row of zeros.
  * 1 <= E <= 1024, E N <= 2^31 - 512, 0 <= R, T <= 2^30 (R = 0 does nothing; with R > 0, T >= 1).
+ * With rows, T ldx < 2^35 (beyond, a call that would gather on the tiles is AWQ_ERR_UNSUPPORTED).
  * ws: with rows, awq_linear_grouped_workspace_bytes(R, E, K) bytes let a large call copy its rows
  * together first, which is faster; NULL (or too small) only does without.  Not to be used by two calls
  * at once.
