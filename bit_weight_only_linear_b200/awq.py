@@ -7,6 +7,7 @@ there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional, Tuple
@@ -139,6 +140,24 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_CURRENT = contextlib.nullcontext()
+_LEGACY = 1             # cudaStreamLegacy: the handle that names the default stream explicitly
+
+
+def _on(stream, device):
+    """Context in which the tensors made for a call belong to the stream that the call runs on.
+
+    The allocator hands a freed block out again at once, for work that follows on the stream the block was
+    made on.  A block made on the current stream and written on another could still be read, or be
+    written, by work queued before."""
+    if stream is None:
+        return _CURRENT
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(0 if handle == _LEGACY else handle, device=device)
+    return torch.cuda.stream(stream)
 
 
 def packed_shapes(N: int, K: int, group_size: int, zero_point: bool):
@@ -322,7 +341,8 @@ def apply_clip(X: torch.Tensor, W: torch.Tensor, s: Optional[torch.Tensor], grou
 # ---------------------------------------------------------------------------
 # Fused and expert-grouped linears, routing and combination.  These four take strided rows and
 # run on the inputs' device (and on its current stream unless one is given), whichever device is
-# current.
+# current.  What they allocate, results and scratch, belongs to the stream that they run on: with a
+# `stream` of its own, other streams wait for it before they use a result, as with any tensor made there.
 # ---------------------------------------------------------------------------
 
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -438,7 +458,8 @@ def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bi
     px, ldx = _rows(X, "X", dev, M, K)
     pr, ldr = _rows(residual, "residual", dev, M, n_out)
     if out is None:
-        out = X.new_empty((M, n_out))
+        with _on(stream, dev):
+            out = X.new_empty((M, n_out))
         py, ldy = out.data_ptr(), n_out
     else:
         py, ldy = _rows(out, "out", dev, M, n_out)
@@ -461,12 +482,9 @@ def _workspace(t: Optional[torch.Tensor], index: int):
 
 
 def _scratch(like: torch.Tensor, need: int, stream) -> torch.Tensor:
-    """Workspace of one call, freed on its return: not to be reused before `stream` has passed it."""
-    ws = like.new_empty(need, dtype=torch.uint8)
-    if stream is not None:
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                         else torch.cuda.ExternalStream(_stream(stream), device=like.device))
-    return ws
+    """Workspace of one call, freed on its return: the call's stream orders its reuse."""
+    with _on(stream, like.device):
+        return like.new_empty(need, dtype=torch.uint8)
 
 
 def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=128, zero_point=True, bias=None,
@@ -489,7 +507,8 @@ def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=12
     R = T if rows is None else rows.shape[0]
     px, ldx = _rows(X, "X", dev, T, K)
     if out is None:
-        out = X.new_empty((R, n_out))
+        with _on(stream, dev):
+            out = X.new_empty((R, n_out))
         py, ldy = out.data_ptr(), n_out
     else:
         py, ldy = _rows(out, "out", dev, R, n_out)
@@ -530,8 +549,9 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
     pl, ld = _rows(logits, "logits", dev, T, E, torch.float16 if half else torch.float32)
     if out is None:
         slots = T * top_k                    # one allocation for the four of that size: most of this call's time
-        made = logits.new_empty_strided((4, T, top_k), (slots, top_k, 1), dtype=torch.int32)
-        offsets = logits.new_empty_strided((E + 1,), (1,), dtype=torch.int32)
+        with _on(stream, dev):
+            made = logits.new_empty_strided((4, T, top_k), (slots, top_k, 1), dtype=torch.int32)
+            offsets = logits.new_empty_strided((E + 1,), (1,), dtype=torch.int32)
         weights, experts, positions, rows = made.unbind()
         out = MoeRoute(weights.view(torch.float32), experts, offsets, rows.flatten(), positions)
         p, step = made.data_ptr(), 4 * slots
@@ -578,7 +598,8 @@ def moe_combine(Y, weights, positions, residual=None, out=None, stream=None) -> 
     py, ldy = _rows(Y, "Y", dev, R, N)
     pr, ldr = _rows(residual, "residual", dev, T, N)
     if out is None:
-        out = Y.new_empty((T, N))
+        with _on(stream, dev):
+            out = Y.new_empty((T, N))
         po, ldo = out.data_ptr(), N
     else:
         po, ldo = _rows(out, "out", dev, T, N)
