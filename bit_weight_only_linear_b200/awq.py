@@ -120,6 +120,16 @@ def config(group_size: int = 128, zero_point: bool = True, w_bit: int = 4) -> Qu
     return QuantConfig(int(w_bit), int(group_size), 1 if zero_point else 0)
 
 
+_CONFIGS = {}
+
+
+def _config(group_size: int, zero_point: bool) -> QuantConfig:
+    c = _CONFIGS.get((group_size, zero_point))
+    if c is None:
+        c = _CONFIGS[(group_size, zero_point)] = config(group_size, zero_point)
+    return c
+
+
 def _dev(t: Optional[torch.Tensor], name: str, dtypes) -> int:
     if t is None:
         return 0
@@ -172,9 +182,10 @@ def quantize_pack(W: torch.Tensor, s: Optional[torch.Tensor] = None, group_size:
     N, K = W.shape
     qs, ss, zs = packed_shapes(N, K, group_size, zero_point)
     if out is None:
-        qweight = torch.empty(qs, dtype=torch.int32, device=W.device)
-        scales = torch.empty(ss, dtype=torch.float16, device=W.device)
-        qzeros = torch.empty(zs, dtype=torch.int32, device=W.device) if zero_point else None
+        with _on(stream, W.device):
+            qweight = torch.empty(qs, dtype=torch.int32, device=W.device)
+            scales = torch.empty(ss, dtype=torch.float16, device=W.device)
+            qzeros = torch.empty(zs, dtype=torch.int32, device=W.device) if zero_point else None
     else:
         qweight, scales, qzeros = out
     st = load_library().awq_quantize_pack(
@@ -188,7 +199,9 @@ def quantize_pack(W: torch.Tensor, s: Optional[torch.Tensor] = None, group_size:
 def fold_inverse_scale(X: torch.Tensor, s: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """awq_fold_inverse_scale: X' = fp16(X / s) per input channel."""
     M, K = X.shape
-    out = torch.empty_like(X) if out is None else out
+    if out is None:
+        with _on(stream, X.device):
+            out = torch.empty_like(X)
     st = load_library().awq_fold_inverse_scale(_dev(X, "X", _F16), _dev(s, "s", _F16), M, K,
                                                _dev(out, "out", _F16), _stream(stream))
     _check("awq_fold_inverse_scale", st)
@@ -200,13 +213,15 @@ def _linear(fn_name: str, X, qweight, scales, qzeros, group_size, zero_point, ou
     N = qweight.shape[0]
     if qweight.shape[1] * 8 != K:
         raise ValueError("qweight must be [N][K/8]")
-    out = torch.empty((M, N), dtype=torch.float16, device=X.device) if out is None else out
+    if out is None:
+        with _on(stream, X.device):
+            out = torch.empty((M, N), dtype=torch.float16, device=X.device)
     ws_ptr, ws_bytes = 0, 0
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     fn = getattr(load_library(), fn_name)
     st = fn(_dev(X, "X", _F16), M, _dev(qweight, "qweight", _W32), _dev(scales, "scales", _F16),
-            _dev(qzeros, "qzeros", _W32), N, K, config(group_size, zero_point), _dev(out, "Y", _F16),
+            _dev(qzeros, "qzeros", _W32), N, K, _config(group_size, zero_point), _dev(out, "Y", _F16),
             ws_ptr, ws_bytes, _stream(stream))
     _check(fn_name, st)
     return out
@@ -221,17 +236,22 @@ def linear_gemv(X, qweight, scales, qzeros, group_size=128, zero_point=True, out
 _GEMM_WS = {}
 
 
-def gemm_workspace(M: int, N: int, K: int, group_size: int = 128, zero_point: bool = True, device=None):
+def gemm_workspace(M: int, N: int, K: int, group_size: int = 128, zero_point: bool = True, device=None, stream=None):
     """A device workspace large enough for awq_linear_gemm at these sizes (the split-K
-    partial sums), cached per device and grown on demand; None when none is needed."""
+    partial sums), cached per device and stream (two streams' calls may overlap) and grown on
+    demand; None when none is needed.  A capture gets one of its own from the graph's pool."""
     need = workspace_bytes(AWQ_OP_GEMM, M, N, K, group_size, zero_point)
     if need == 0:
         return None
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    ws = _GEMM_WS.get(dev)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _GEMM_WS[dev] = ws
+    dev = device if isinstance(device, torch.device) else torch.device("cuda" if device is None else device)
+    with _on(stream, dev):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+        index = torch.cuda.current_device() if dev.index is None else dev.index
+        key = index, torch._C._cuda_getCurrentRawStream(index)
+        ws = _GEMM_WS.get(key)
+        if ws is None or ws.numel() < need:
+            ws = _GEMM_WS[key] = torch.empty(need, dtype=torch.uint8, device=dev)
     return ws
 
 
@@ -241,12 +261,19 @@ def linear_gemm(X, qweight, scales, qzeros, group_size=128, zero_point=True, out
     batch too small to fill the GPU splits K over a workspace (the cached one of
     gemm_workspace() unless one is given)."""
     if workspace is None:
-        workspace = gemm_workspace(X.shape[0], qweight.shape[0], X.shape[1], group_size, zero_point, X.device)
+        workspace = gemm_workspace(X.shape[0], qweight.shape[0], X.shape[1], group_size, zero_point, X.device, stream)
     return _linear("awq_linear_gemm", X, qweight, scales, qzeros, group_size, zero_point, out, workspace, stream)
 
 
 def workspace_bytes(op: int, M: int, N: int, K: int, group_size: int = 128, zero_point: bool = True) -> int:
-    return int(load_library().awq_workspace_bytes(op, M, N, K, config(group_size, zero_point)))
+    return int(load_library().awq_workspace_bytes(op, M, N, K, _config(group_size, zero_point)))
+
+
+def _search_outputs(X: torch.Tensor, n_grid: int, stream):
+    with _on(stream, X.device):
+        return (torch.empty(X.shape[1], dtype=torch.float16, device=X.device),
+                torch.empty(n_grid, dtype=torch.float64, device=X.device),
+                torch.empty(1, dtype=torch.int32, device=X.device))
 
 
 def scale_search(X: torch.Tensor, W: torch.Tensor, group_size: int = 128, zero_point: bool = True,
@@ -259,13 +286,9 @@ def scale_search(X: torch.Tensor, W: torch.Tensor, group_size: int = 128, zero_p
     N = W.shape[0]
     if workspace is None:
         need = workspace_bytes(AWQ_OP_SCALE_SEARCH, M, N, K, group_size, zero_point)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
-    if out is None:
-        s_out = torch.empty(K, dtype=torch.float16, device=X.device)
-        losses = torch.empty(n_grid, dtype=torch.float64, device=X.device)
-        best = torch.empty(1, dtype=torch.int32, device=X.device)
-    else:
-        s_out, losses, best = out
+        with _on(stream, X.device):
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+    s_out, losses, best = _search_outputs(X, n_grid, stream) if out is None else out
     name = "awq_scale_search_duo" if duo_scaling else "awq_scale_search"
     st = getattr(load_library(), name)(
         _dev(X, "X", _F16), M, _dev(W, "W", _F16), N, K, config(group_size, zero_point), n_grid,
@@ -282,12 +305,7 @@ def scale_search_noalloc(X: torch.Tensor, W: torch.Tensor, group_size: int = 128
     device, into `out` when given (otherwise torch allocates them here, for convenience)."""
     M, K = X.shape
     N = W.shape[0]
-    if out is None:
-        s_out = torch.empty(K, dtype=torch.float16, device=X.device)
-        losses = torch.empty(n_grid, dtype=torch.float64, device=X.device)
-        best = torch.empty(1, dtype=torch.int32, device=X.device)
-    else:
-        s_out, losses, best = out
+    s_out, losses, best = _search_outputs(X, n_grid, stream) if out is None else out
     st = load_library().awq_scale_search_noalloc(
         _dev(X, "X", _F16), M, _dev(W, "W", _F16), N, K, config(group_size, zero_point), n_grid,
         _dev(s_out, "s_out", _F16), losses.data_ptr(), best.data_ptr(), _stream(stream))
@@ -317,16 +335,18 @@ def apply_clip(X: torch.Tensor, W: torch.Tensor, s: Optional[torch.Tensor], grou
     lib = load_library()
     if workspace is None:
         need = int(lib.awq_apply_clip_workspace_bytes(M, N, K, config(group_size, zero_point), n_clip))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+        with _on(stream, X.device):
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
     qs, ss, zs = packed_shapes(N, K, group_size, zero_point)
-    if out is None:
-        qweight = torch.empty(qs, dtype=torch.int32, device=W.device)
-        scales = torch.empty(ss, dtype=torch.float16, device=W.device)
-        qzeros = torch.empty(zs, dtype=torch.int32, device=W.device) if zero_point else None
-        idx = torch.empty((N, K // group_size), dtype=torch.uint8, device=W.device)
-    else:
-        qweight, scales, qzeros, idx = out
-    err = torch.empty((N, K // group_size, n_clip), dtype=torch.float64, device=W.device) if errors else None
+    with _on(stream, W.device):
+        if out is None:
+            qweight = torch.empty(qs, dtype=torch.int32, device=W.device)
+            scales = torch.empty(ss, dtype=torch.float16, device=W.device)
+            qzeros = torch.empty(zs, dtype=torch.int32, device=W.device) if zero_point else None
+            idx = torch.empty((N, K // group_size), dtype=torch.uint8, device=W.device)
+        else:
+            qweight, scales, qzeros, idx = out
+        err = torch.empty((N, K // group_size, n_clip), dtype=torch.float64, device=W.device) if errors else None
     st = lib.awq_apply_clip(
         _dev(X, "X", _F16), M, _dev(W, "W", _F16), _dev(s, "s", _F16), N, K, config(group_size, zero_point),
         n_grid, n_clip, _dev(qweight, "qweight", _W32), _dev(scales, "scales", _F16), _dev(qzeros, "qzeros", _W32),
@@ -347,14 +367,6 @@ def apply_clip(X: torch.Tensor, W: torch.Tensor, s: Optional[torch.Tensor], grou
 
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORINGS = {"softmax": 0, "sigmoid": 1}
-_CONFIGS = {}
-
-
-def _config(group_size: int, zero_point: bool) -> QuantConfig:
-    c = _CONFIGS.get((group_size, zero_point))
-    if c is None:
-        c = _CONFIGS[(group_size, zero_point)] = config(group_size, zero_point)
-    return c
 
 
 def _refuse(t, name, index, shape, dtypes, what):
@@ -409,6 +421,11 @@ _linear_fused, _linear_grouped, _moe_route, _moe_combine = map(
     _entry, ("awq_linear_fused", "awq_linear_grouped", "awq_moe_route", "awq_moe_combine"))
 
 
+def _empty(like: torch.Tensor, shape, stream, dtype=None) -> torch.Tensor:
+    with _on(stream, like.device):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _cuda(t: torch.Tensor, name: str, dims: int = 2):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -458,8 +475,7 @@ def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bi
     px, ldx = _rows(X, "X", dev, M, K)
     pr, ldr = _rows(residual, "residual", dev, M, n_out)
     if out is None:
-        with _on(stream, dev):
-            out = X.new_empty((M, n_out))
+        out = X.new_empty((M, n_out)) if stream is None else _empty(X, (M, n_out), stream)
         py, ldy = out.data_ptr(), n_out
     else:
         py, ldy = _rows(out, "out", dev, M, n_out)
@@ -479,12 +495,6 @@ def _workspace(t: Optional[torch.Tensor], index: int):
     if t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on cuda:{index}")
     return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _scratch(like: torch.Tensor, need: int, stream) -> torch.Tensor:
-    """Workspace of one call, freed on its return: the call's stream orders its reuse."""
-    with _on(stream, like.device):
-        return like.new_empty(need, dtype=torch.uint8)
 
 
 def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=128, zero_point=True, bias=None,
@@ -507,15 +517,14 @@ def linear_grouped(X, qweight, scales, qzeros, offsets, rows=None, group_size=12
     R = T if rows is None else rows.shape[0]
     px, ldx = _rows(X, "X", dev, T, K)
     if out is None:
-        with _on(stream, dev):
-            out = X.new_empty((R, n_out))
+        out = X.new_empty((R, n_out)) if stream is None else _empty(X, (R, n_out), stream)
         py, ldy = out.data_ptr(), n_out
     else:
         py, ldy = _rows(out, "out", dev, R, n_out)
     if workspace is None and R >= _GATHER_MIN_SHARE * E and rows is not None:
         need = (_lib or load_library()).awq_linear_grouped_workspace_bytes(R, E, K)
         if need:
-            workspace = _scratch(X, need, stream)
+            workspace = _empty(X, need, stream, torch.uint8)
     ws, ws_bytes = _workspace(workspace, dev)
     _linear_grouped(dev, stream, px, T, ldx, _flat(rows, "rows", dev, (R,), _I32), R,
         _flat(offsets, "offsets", dev, (E + 1,), _I32), E, pq, ps, pz, N, K, _config(group_size, zero_point),
@@ -565,7 +574,7 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
     if workspace is None:
         need = _route_need(T, E, dev)
         if need:
-            workspace = _scratch(logits, need, stream)
+            workspace = _empty(logits, need, stream, torch.uint8)
     ws, ws_bytes = _workspace(workspace, dev)
     _moe_route(dev, stream, pl, 1 if half else 0, T, ld, E, top_k, score, 1 if renormalize else 0, *pointers, ws,
                ws_bytes)
@@ -598,8 +607,7 @@ def moe_combine(Y, weights, positions, residual=None, out=None, stream=None) -> 
     py, ldy = _rows(Y, "Y", dev, R, N)
     pr, ldr = _rows(residual, "residual", dev, T, N)
     if out is None:
-        with _on(stream, dev):
-            out = Y.new_empty((T, N))
+        out = Y.new_empty((T, N)) if stream is None else _empty(Y, (T, N), stream)
         po, ldo = out.data_ptr(), N
     else:
         po, ldo = _rows(out, "out", dev, T, N)

@@ -95,11 +95,13 @@ def fakes(monkeypatch):
     monkeypatch.setattr(awq, "_lib", Library())
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: SimpleNamespace(cuda_stream=h))
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: SimpleNamespace(cuda_stream=log.current))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: log.current, raising=False)
     monkeypatch.setattr(torch, "empty", lambda *shape, dtype=None, device=None: Fake(log, (0,), torch.uint8).new_empty(
         shape[0] if isinstance(shape[0], (tuple, list)) else shape, dtype))
+    monkeypatch.setattr(torch, "empty_like", lambda x: x.new_empty(x.shape))
 
     def tensor(*shape, dtype=torch.float16):
         return Fake(log, shape, dtype)
@@ -131,6 +133,47 @@ def test_allocations_of_the_fused_operators_belong_to_the_stream(fakes, name, st
     want = 0 if stream is None else stream
     assert [s for _, s in log.made] == [want] * NEW[name]
     assert calls == [("awq_" + name, want)]
+
+
+def _older_calls(awq, t, stream):
+    X, W = t(64, 256), t(64, 256)
+    w = (t(64, 32, dtype=torch.int32), t(64, 2), t(64, 1, dtype=torch.int32))
+    return {
+        "quantize_pack": lambda: awq.quantize_pack(W, None, 128, True, stream=stream),
+        "fold_inverse_scale": lambda: awq.fold_inverse_scale(X, t(256), stream=stream),
+        "linear_gemv": lambda: awq.linear_gemv(t(4, 256), *w, 128, True, stream=stream),
+        "linear_gemm": lambda: awq.linear_gemm(X, *w, 128, True, stream=stream),
+        "scale_search": lambda: awq.scale_search(X, W, 128, True, stream=stream),
+        "scale_search_noalloc": lambda: awq.scale_search_noalloc(X, W, 128, True, stream=stream),
+        "apply_clip": lambda: awq.apply_clip(X, W, None, 128, True, stream=stream, errors=True),
+    }
+
+
+OLDER = {"quantize_pack": 3, "fold_inverse_scale": 1, "linear_gemv": 1, "linear_gemm": 2, "scale_search": 4,
+         "scale_search_noalloc": 3, "apply_clip": 6}
+
+
+@pytest.mark.parametrize("name", OLDER)
+@pytest.mark.parametrize("stream", [SIDE, 0, None])
+def test_allocations_of_the_other_calls_belong_to_the_stream(fakes, monkeypatch, name, stream):
+    awq, log, t, calls = fakes
+    monkeypatch.setattr(awq, "_GEMM_WS", {})
+    log.current = 0 if stream is None else 0x9000
+    _older_calls(awq, t, stream)[name]()
+    want = 0 if stream is None else stream
+    assert [s for _, s in log.made] == [want] * OLDER[name]
+    assert calls == [("awq_" + name, want)]
+
+
+def test_gemm_workspaces_of_two_streams_differ(fakes, monkeypatch):
+    awq, log, t, _ = fakes
+    monkeypatch.setattr(awq, "_GEMM_WS", {})
+    a, b, again = (awq.gemm_workspace(64, 64, 256, stream=s, device=0) for s in (SIDE, 0, SIDE))
+    assert a is not b and again is a
+    # a captured call's belongs to its graph: neither kept nor taken from the eager calls
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    c, d = (awq.gemm_workspace(64, 64, 256, stream=SIDE, device=0) for _ in range(2))
+    assert c is not a and c is not d and len(awq._GEMM_WS) == 2
 
 
 # ---------------------------------------------------------------------------
@@ -195,3 +238,48 @@ def test_calls_on_a_side_stream_leave_the_current_streams_blocks(lib):
     lib.device_error()
     assert all((a == 7).all() for a in kept)
     assert all(torch.equal(a, b) for a, b in zip(r, r0)) and torch.equal(y, y0) and torch.equal(c, c0)
+
+
+@pytest.mark.gpu
+def test_two_batches_on_two_streams_with_split_sums(lib):
+    """linear_gemm splits K over a workspace: overlapping calls of two streams do not share it."""
+    N, K, G = 512, 4096, 128
+    w = R.packed(8, N, K, G, True)
+    X = [R.activations(9 + i, 64, K) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in X]
+    want = [lib.linear_gemm(x, *w, G, True) for x in X]
+    assert lib.gemm_workspace(64, N, K, G, True) is not None
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            outs[i].append(lib.linear_gemm(X[i], *w, G, True, stream=s))
+    torch.cuda.synchronize()
+    lib.device_error()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in outs[i])
+
+
+@pytest.mark.gpu
+def test_two_captured_batches_replayed_at_once(lib):
+    """Graphs of split products, one of each stream and an eager call beside them."""
+    N, K, G = 512, 4096, 128
+    w = R.packed(8, N, K, G, True)
+    X = [R.activations(11 + i, 64, K) for i in range(3)]
+    want = [lib.linear_gemm(x, *w, G, True) for x in X]
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(lib.linear_gemm(X[i], *w, G, True))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = lib.linear_gemm(X[2], *w, G, True)
+    torch.cuda.synchronize()
+    lib.device_error()
+    assert torch.equal(eager, want[2]) and all(torch.equal(o, y) for o, y in zip(outs, want))
