@@ -56,6 +56,16 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
+// Sigmoid score e^l / (1 + e^l), times e^-shift; no exponential overflows.  Scores that are divided by their
+// sum are taken relative to the token's largest logit where that is negative (shift = min(top, 0)): below -87 the
+// scores themselves are denormals, below -104 nothing in fp32, while their shares are ordinary numbers.  A
+// logit from kLowestScored down scores 0, so that a lowest finite value written as a mask gives no weight.
+constexpr float kLowestScored = -700.0f;
+
+__device__ __forceinline__ float sigmoid_score(float l, float shift) {
+    return l > kLowestScored ? expf(fminf(l, 0.0f) - shift) / (1.0f + expf(-fabsf(l))) : 0.0f;
+}
+
 // Exclusive prefix sum of cnt[0..E) into base[0..E], by the whole block (E <= kRouteThreads).
 __device__ __forceinline__ void block_prefix(const int* cnt, int* base, int E, int* warp_sums) {
     const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
@@ -184,7 +194,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
             float v = 0.0f;
             if (chosen >= 0) {
                 const float l = fminf(key_logit(chosen_key), 3.402823466e38f);
-                v = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - lmax);
+                v = a.sigmoid ? sigmoid_score(l, a.renorm ? fminf(lmax, 0.0f) : 0.0f) : expf(l - lmax);
                 if (!a.sigmoid && !a.renorm) v /= total;
             }
             if (a.renorm) {
@@ -365,7 +375,7 @@ __global__ void __launch_bounds__(kRouteWalkThreads) route_walk_kernel(RouteArgs
                 if (s == q * kOwn + i && s < a.k) k = key[s], own[i] = pick[s];
             if (k) {
                 const float l = fminf(key_logit(k), 3.402823466e38f);
-                w[i] = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - lmax);
+                w[i] = a.sigmoid ? sigmoid_score(l, a.renorm ? fminf(lmax, 0.0f) : 0.0f) : expf(l - lmax);
                 if (!a.sigmoid && !a.renorm) w[i] /= total;
             }
             sum += w[i];

@@ -291,9 +291,10 @@ enum { AWQ_SCORE_SOFTMAX = 0, AWQ_SCORE_SIGMOID = 1 };
  * expert first):
  *   experts[t][j]    the expert, or -1 where only masked experts are left.  An expert is masked by
  *                    a logit of -inf (or NaN); the lowest finite value is an ordinary logit.
- *   weights[t][j]    fp32 softmax over the unmasked experts (sigmoid: of its logit), with
- *                    renormalize = 1 divided by the sum over the token's slots; 0 for expert -1
- *                    and where that sum is 0.  A logit of +inf counts as the largest finite fp32.
+ *   weights[t][j]    fp32 softmax over the unmasked experts (sigmoid: of its logit; a logit from -700
+ *                    down scores 0), with renormalize = 1 divided by the sum over the token's slots (no
+ *                    score is too small for that); 0 for expert -1 and where that sum is 0.  A logit of
+ *                    +inf counts as the largest finite fp32.
  *   offsets [E+1]    rows offsets[e] .. offsets[e+1]-1 belong to expert e, in token order
  *   rows [T top_k]   the token of each row, -1 behind the last expert's rows
  *   positions[t][j]  the row of the slot, or -1 for expert -1
