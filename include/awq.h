@@ -245,9 +245,18 @@ enum {
  * rows in elements; ldx a multiple of 8 (X 16-byte aligned as ever), while bias, residual
  * and Y need only their element's alignment.  N need not be a multiple of anything.
  * M <= 2^30, N <= 2^31 - 512.
- * Needs no workspace.  Range: a batch on the tensor-core tiles (always above 16 rows; grouped, also few
- * rows of each of many experts) rounds each dequantised weight once to fp16 and reports AWQ_ERR_RANGE as
- * awq_linear_gemm does; other calls multiply codes and scales exactly and have no such limit.
+ * Needs no workspace.  Two forms take the calls, and the form sets rounding and range:
+ *   - few rows: codes and scales are multiplied exactly, without a limit.  K is a multiple of 128, and M <= 8,
+ *     or M <= 16 where N K <= 2^27.  The rows, at once or, where N K <= 2^27, in two halves, have to fit in
+ *     shared memory: for every group size they do up to K = 59392 for 1 row at a time, 28672 for 2, 12288 for
+ *     4 and 4096 for 8 (halves of 9 to 16 rows: 2048 for 8).  Grouped: at most 8 rows on average for each of
+ *     min(R, E) experts, all of an average fitting at once, and not many experts of few rows each where the
+ *     other form is the faster one.
+ *   - the tensor-core tiles take all other calls.  They round each dequantised weight once to fp16 and report
+ *     AWQ_ERR_RANGE as awq_linear_gemm does.
+ * An infinity or NaN in a row of X stays in that row of Y.  On the tiles infinities come out as the sums
+ * above give them; in the form for few rows, which subtracts the zero points' share from the codes', such a
+ * row's acc is NaN throughout.
  * Ordering: as awq_linear_gemv, a call may read the weights before the previous kernel on `stream` has
  * completed, so that kernel must not write them (the quantisers end with an ordering kernel of theirs).
  */
