@@ -276,9 +276,11 @@ awq_status awq_scale_search_noalloc(const uint16_t* X, int32_t M, const uint16_t
 
 namespace {
 
-// Rows of X and weight rows (of all experts) that the kernels' 32-bit indexes and tile coordinates hold.
+// Rows of X, weight rows (of all experts) and their length that the kernels' 32-bit indexes and tile
+// coordinates hold.
 constexpr int kFusedMaxRows = 1 << 30;
 constexpr int kFusedMaxN = 0x7ffffe00;
+constexpr int kFusedMaxK = 0x7ffffe00;
 
 // Checks shared by the fused and the grouped linear; the row counts may be 0.
 awq_status check_fused(const uint16_t* X, int M, int64_t ldx, const uint32_t* qweight, const uint16_t* scales,
@@ -291,7 +293,7 @@ awq_status check_fused(const uint16_t* X, int M, int64_t ldx, const uint32_t* qw
     if (st != AWQ_OK) return st;
     if (M < 0 || activation < AWQ_ACT_NONE || activation > AWQ_ACT_GELU_TANH || (gated != 0 && gated != 1))
         return AWQ_ERR_INVALID_ARG;
-    if (M > kFusedMaxRows || N > kFusedMaxN) return AWQ_ERR_UNSUPPORTED;
+    if (M > kFusedMaxRows || N > kFusedMaxN || K > kFusedMaxK) return AWQ_ERR_UNSUPPORTED;
     if (gated && (N & 1)) return AWQ_ERR_INVALID_ARG;
     const int64_t n_out = gated ? N / 2 : N;
     if (ldx < K || (ldx & 7) || ldy < n_out || (residual && ldr < n_out)) return AWQ_ERR_INVALID_ARG;
@@ -382,7 +384,7 @@ awq_status awq_moe_combine(const uint16_t* Y, int32_t R, int64_t ldy, const floa
                            int32_t T, int32_t top_k, int32_t N, const uint16_t* residual, int64_t ldr, uint16_t* out,
                            int64_t ldo, void* stream) {
     if (R < 0 || T < 0 || top_k < 1 || N < 1 || ldy < N || ldo < N || (residual && ldr < N)) return AWQ_ERR_INVALID_ARG;
-    if (ceil_div(N, kCombineThreads) > 65535) return AWQ_ERR_UNSUPPORTED;
+    if (N > 65535 * kCombineThreads) return AWQ_ERR_UNSUPPORTED;
     if (T == 0) return AWQ_OK;
     if ((R && !Y) || !weights || !positions || !out || !aligned4(weights) || !aligned4(positions))
         return AWQ_ERR_INVALID_ARG;

@@ -244,7 +244,7 @@ enum {
  * not overlap any other input.  Rows may be strided: ldx, ldr, ldy are the distances of
  * rows in elements; ldx a multiple of 8 (X 16-byte aligned as ever), while bias, residual
  * and Y need only their element's alignment.  N need not be a multiple of anything.
- * M <= 2^30, N <= 2^31 - 512.
+ * M <= 2^30, N and K <= 2^31 - 512.
  * Needs no workspace.  Two forms take the calls, and the form sets rounding and range:
  *   - few rows: codes and scales are multiplied exactly, without a limit.  K is a multiple of 128, and M <= 8,
  *     or M <= 16 where N K <= 2^27.  The rows, at once or, where N K <= 2^27, in two halves, have to fit in
@@ -275,7 +275,7 @@ awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uin
  * The tables are read by the kernel, so the call neither synchronises nor depends on their
  * values at capture.  Entries beyond the limits never read or write out of bounds: offsets
  * are clamped to 0 .. R, and a row number outside 0 .. T-1 counts as a row of zeros.
- * 1 <= E <= 1024, E N <= 2^31 - 512, 0 <= R, T <= 2^30 (R = 0 does nothing; with R > 0, T >= 1).
+ * 1 <= E <= 1024, E N and K <= 2^31 - 512, 0 <= R, T <= 2^30 (R = 0 does nothing; with R > 0, T >= 1).
  * With rows, T ldx < 2^35 (beyond, a call that would gather on the tiles is AWQ_ERR_UNSUPPORTED).
  * ws: with rows, awq_linear_grouped_workspace_bytes(R, E, K) bytes let a large call copy its rows
  * together first, which is faster; NULL (or too small) only does without.  Not to be used by two calls
@@ -323,8 +323,8 @@ size_t awq_moe_route_workspace_bytes(int32_t T, int32_t E);
  * Combination of a token's expert rows: out[t][n] = fp16( residual[t][n] +
  * sum_j weights[t][j] Y[positions[t][j]][n] ), fp32 sums in slot order.  A position outside
  * 0 .. R-1 contributes nothing (its weight is not read).  residual [T][ldr] may be NULL, and may
- * be out itself; out must not overlap Y.  Any T >= 0, top_k >= 1, N >= 1; rows may be strided,
- * 2-byte aligned.
+ * be out itself; out must not overlap Y.  Any T >= 0, top_k >= 1, 1 <= N <= 65535 x 128; rows may be
+ * strided, 2-byte aligned.
  */
 awq_status awq_moe_combine(const uint16_t* Y, int32_t R, int64_t ldy, const float* weights,
                            const int32_t* positions, int32_t T, int32_t top_k, int32_t N,
