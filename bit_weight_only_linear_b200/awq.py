@@ -485,7 +485,7 @@ def linear_fused(X, qweight, scales, qzeros, group_size=128, zero_point=True, bi
 
 
 _I32 = (torch.int32,)
-_GATHER_MIN_SHARE = 64   # rows per expert below which a grouped call asks for no workspace
+_GATHER_MIN_SHARE = 64   # kGatherMinShare: rows per expert below which a grouped call needs no workspace
 
 
 def _workspace(t: Optional[torch.Tensor], index: int):
@@ -582,7 +582,7 @@ def moe_route(logits, top_k: int, scoring: str = "softmax", renormalize: bool = 
 
 
 _F32 = (torch.float32,)
-_ROUTE_SINGLE = 32      # tokens up to which routing is one block and needs no workspace
+_ROUTE_SINGLE = 32      # kRouteSingle: tokens up to which routing is one block and needs no workspace
 
 
 def _route_need(T: int, E: int, index: int) -> int:

@@ -278,8 +278,8 @@ awq_status awq_linear_fused(const uint16_t* X, int32_t M, int64_t ldx, const uin
  * 1 <= E <= 1024, E N and K <= 2^31 - 512, 0 <= R, T <= 2^30 (R = 0 does nothing; with R > 0, T >= 1).
  * With rows, T ldx < 2^35 (beyond, a call that would gather on the tiles is AWQ_ERR_UNSUPPORTED).
  * ws: with rows, awq_linear_grouped_workspace_bytes(R, E, K) bytes let a large call copy its rows
- * together first, which is faster; NULL (or too small) only does without.  Not to be used by two calls
- * at once.
+ * together first, which is faster; NULL (or too small) only does without, while a ws that is not 16-byte
+ * aligned is AWQ_ERR_INVALID_ARG like any other such pointer.  Not to be used by two calls at once.
  */
 awq_status awq_linear_grouped(const uint16_t* X, int32_t T, int64_t ldx, const int32_t* rows, int32_t R,
                               const int32_t* offsets, int32_t E, const uint32_t* qweight,
