@@ -19,9 +19,12 @@
 //   * Warps: a producer (3-D TMA, 32 KB stages of 32 rows x 2048 codes), two converters (scales and
 //     zeros -> fp32 pairs per stage), 16 consumers (128 codes of a stage each), a reducer for each 32
 //     rows of the unit (the consumers' partial sums in a fixed order, then the epilogue).
-// Bound: HBM where CTAs get many units (8 tokens, 2 of 8 experts, 28672 x 4096: 80 us = 5.5 TB/s, 0.84 of the
-// measured copy rate); for one dense matrix the start and end of a launch, about 4 us, and the uneven last
-// unit (1 row x 28672 x 4096, gated: 15.6 us = 3.9 TB/s; 4096 x 4096: 4.8 us).
+// Bound: HBM where CTAs get many units (8 tokens, 2 of 8 experts, 28672 x 4096: 367 MB of the 6 experts touched
+// in 69.7 us = 5.26 TB/s, 0.80 of the measured copy rate); for one dense matrix the start and end of a launch,
+// about 4 us, and the uneven last unit (1 row x 28672 x 4096, gated: 15.2 us = 4.0 TB/s; 4096 x 4096: 4.7 us).
+// The GEMV, without an epilogue, is 4 to 8 % faster at one row (13.4 against 14.5 us for 28672 x 4096, 4.35
+// against 4.7 for 4096 x 4096: two CTAs an SM and 16-row units) and slower from 2 to 4 rows on (8 rows: 19.9
+// against 16.9, 8.0 against 6.8).
 // K must be a multiple of 128.  Every wait is bounded.
 #pragma once
 
@@ -42,7 +45,7 @@ constexpr int dec_threads(int RS) { return (kDecReducer0 + RS + kDecConsumers) *
 constexpr int kDecRows = 32;                     // weight rows of a consumer: two MMA row tiles
 constexpr int kDecStageBytes = 32 * 1024;        // 32 RS rows x 2048 / RS codes
 constexpr int kDecMaxRows = 8;                   // rows of X at a time (MMA N)
-constexpr int kDecManyUnits = 8;                 // 32-row units per CTA from which a unit is 64 rows
+constexpr int kDecManyUnits = 8;                 // 32-row units (gated: pairs of them) per CTA from which a unit is 64 rows
 constexpr int kDecMaxSegs = 32;                  // segments of a CTA
 constexpr int kDecMaxK = 1 << 17;                // (no row of X beyond it fits in shared memory)
 constexpr int kDecPartPitch = 36;                // words per row of X in a partial sum (bank spread)
@@ -594,7 +597,13 @@ inline bool experts_prefer_tiles(const LinearArgs& l, int sms, int mc) {
 // against 20).
 inline awq_status launch_linear(const LinearArgs& l, const DeviceInfo& d, cudaStream_t st) {
     const int share = l.offsets ? ceil_div(l.R, std::min(l.R, l.E)) : l.R;
-    // 64-row units where every CTA gets many, however the units fall (and a stage has 8 groups per row)
+    // 64-row units where every CTA gets many (and a stage has 8 groups per row): half as many partial sums meet,
+    // but the last round of units is twice as long.  Gated, pairs are counted, so the change comes at 16.  32-row
+    // against 64-row units, us, 1 / 8 rows: 28672 x 4096 (6 a CTA) 15.1 / 17.6 against 15.4 / 18.2; 37888 x 4096 (8)
+    // 17.6 / 20.8 against 17.1 / 20.1; 37888 x 2048, G = 64 13.5 / 16.7 against 12.8 / 13.6; 57344 x 4096 gated (12)
+    // 24.4 / 28.5 against 24.6 / 29.0, 75776 x 4096 gated (16) 29.8 / 34.1 against 29.6 / 33.8; 3 rows each of 64 experts,
+    // 2816 x 2048 gated (38) 58.9 against 39.4.  Below the limit 64 rows win at short K only: 18944 x 2048, G = 64 (4)
+    // 8.7 / 10.9 against 8.4 / 9.4.
     const long long units = (long long)(l.offsets ? std::min(l.R, l.E) : 1) * ceil_div(l.ep.gated ? l.N / 2 : l.N, 32);
     const int RS = l.G <= 128 && units >= (long long)kDecManyUnits * d.sms ? 2 : 1;
     const int passes = l.offsets || share <= 1 || (long long)l.N * l.K > (128LL << 20) ? 1 : 2;

@@ -21,14 +21,18 @@
 //     distributed shared memory and are added in rank order (no workspace, no second kernel).
 //   * Grouped: every expert's rows are cut into tiles of their own; a CTA finds its tile by a scan
 //     over the offsets table, so nothing is read back to the host.
-// Bound: the tensor cores from about 150 rows on (2048 rows x 57344 x 8192, gated: 1.33 ms = 1450 TFLOP/s,
-// 0.87 of the measured burst rate, above the sustained one); the round trip between conversion and MMA,
+// Bound: the tensor cores from about 150 rows on (2048 rows x 57344 x 8192, gated: 1.32 to 1.34 ms in a short graph =
+// 1430 to 1460 TFLOP/s, 0.87 of the measured burst rate; call after call, at the clocks the power cap leaves, 1.52 ms
+// = 1270, 0.92 of the sustained rate); the round trip between conversion and MMA,
 // 0.3 us per 64 codes of 256 rows, below (61 rows x 4096 x 14336: 24 us, of which 8 are the start and the
 // exchange of the splits); with tiles of few rows the issue of the conversion (96 tokens, 6 of 64 experts,
 // 2816 x 2048: 62 us = 3.2 TB/s).
-// Each dequantised weight is rounded once to fp16, as in awq_linear_gemm, whose range flag it
-// raises too.  Every wait is bounded: on time-out the kernel raises the device error word, drains
-// what it issued, frees TMEM and returns.
+// Each dequantised weight is rounded once to fp16, as in awq_linear_gemm, whose range flag it raises too: (q - z) *
+// scale has 15 significant bits, the MMA's fp16 operand 11.  To keep them all would take a second MMA for the
+// remainders, or unscaled codes as the operand and the 256 x BN sums read back and scaled after every group.  The
+// error against 64 bits is 2.7e-4 (rms, relative; gated 3.3e-4), of which the output's own rounding is 2.1e-4; sums
+// are fp32.  Every wait is bounded: on time-out the kernel raises the device error word, drains what it issued,
+// frees TMEM and returns.
 #pragma once
 
 #include <algorithm>
@@ -860,7 +864,8 @@ inline awq_status launch_linear_tc(const LinearArgs& l, int sms, cudaStream_t st
     // 2048: 62 us at 32 rows a tile against 92 with one CTA; with fewer tiles than SMs it is the reverse,
     // 16 tiles of 61 rows x 14336 in 6 parts: 24 us against 28).  A tile holds 2.2 times the experts' average,
     // since a second tile reads an expert's weights again (the same experts at tiles of 16 / 32 / 64 rows, 6 rows
-    // each: 61 / 62 / 65 us, 9: 65 / 62 / 65, 12: 69 / 63 / 66, 16: 78 / 67 / 67, 19: 87 / 71 / 67).
+    // each: 61 / 62 / 65 us, 9: 65 / 62 / 65, 12: 69 / 63 / 66, 16: 78 / 67 / 67, 19: 87 / 71 / 67).  Skewed shares, 9 rows
+    // on average: one expert with 96 62 us, two with 96 68; 8 on average: one with 256 of 512 rows 70.
     if (m <= 64 && 2LL * active * n_tiles >= 3LL * sms) {
         const long long hold = l.offsets ? ((long long)l.R * 11 + active * 5 - 1) / (active * 5) : l.R;
         if (hold <= 16) return launch_tc_bn<16>(l, 1, st);
