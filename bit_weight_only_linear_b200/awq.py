@@ -4,6 +4,10 @@ Every computation happens in the CUDA library: this module checks dtypes and
 shapes, takes data pointers and the current CUDA stream from torch tensors, and
 calls the entry point of the same name.  It raises if the library is missing:
 there is no CPU fallback.
+
+Results and scratch that a call allocates belong to the stream that it runs on (`stream`, or the current
+one): before another stream uses a result it waits for that stream, and tells the allocator
+(`Tensor.record_stream`), as for any tensor made there.
 """
 from __future__ import annotations
 
